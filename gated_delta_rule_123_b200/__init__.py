@@ -30,6 +30,11 @@ SYMBOLS = (
     "kda_dplr_chunk_fwd_workspace", "kda_dplr_chunk_fwd", "kda_recurrent_bwd_workspace", "kda_recurrent_bwd",
     "kda_chunk_fwd_segment_tokens", "kda_chunk_fwd_workspace_min", "kda_debug_fault_injection",
     "kda_linear_bf16", "kda_chunk_fwd_plan_items",
+    "kda_layer_norm_fwd", "kda_layer_norm_bwd_workspace", "kda_layer_norm_bwd",
+    "kda_linear_act_bf16", "kda_linear_act_bwd_workspace", "kda_linear_act_bwd_bf16",
+    "kda_short_conv_fwd", "kda_short_conv_bwd_workspace", "kda_short_conv_bwd", "kda_short_conv_step",
+    "kda_selective_scan_fwd_workspace", "kda_selective_scan_fwd", "kda_selective_scan_bwd_workspace",
+    "kda_selective_scan_bwd", "kda_selective_scan_step",
 )
 
 
@@ -376,3 +381,8 @@ def layer_decode(x, packed: dict, conv_state, state, out=None, workspace=None):
                                _ptr(workspace), wsz, _stream(x.device))
     _check(rc, "kda_layer_decode")
     return y
+
+
+from .mixer import (  # noqa: E402  (needs _lib and _check)
+    layer_norm_fwd, layer_norm_bwd, linear_act, linear_act_bwd, short_conv_fwd, short_conv_bwd, short_conv_step,
+    selective_scan_fwd, selective_scan_bwd, selective_scan_step)

@@ -16,6 +16,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
     "-Xptxas", "-v",
+    "--split-compile=0",  # the kernels of the one translation unit on all cores
 ]
 
 

@@ -1,0 +1,537 @@
+// Short causal depthwise convolution, the public form of the layer's ShortConv
+// ("Kimi Linear: An Expressive, Efficient Attention Architecture", section "Neural
+// Parameterization"), with a bias, gradients and a single-token step.
+//
+//   s_t = b + sum_j w_j x_{t-(W-1)+j},  y_t = SiLU(s_t) or s_t
+//   with ds = dy SiLU'(s):  dx_t = sum_j w_j ds_{t+(W-1)-j},  dw_j = sum_t ds_t x_{t-(W-1)+j},  db = sum_t ds_t
+//
+// The inputs before a sequence's start come from its cache of W - 1 rows, oldest
+// first, or are zero.  Dense batches and packed sequences are one axis of tokens,
+// on which the window restarts at each sequence.  Bound by HBM: forward reads x
+// and writes y, backward reads dy and x and writes dx.  A thread owns one 16-byte
+// vector of channels and slides over a run of tokens, so each row is read once
+// but for the W - 1 rows next to the run.
+#include "kda_mixer.cuh"
+
+namespace kda {
+
+namespace conv {  // seq_of and seq_begin (the sequence of a token, its first token) are the layer's
+
+using namespace mix;
+
+struct Args {
+    const void *x, *w, *cache_in;
+    const float* bias;
+    void *y, *cache_out;
+    const int32_t* cu;
+    long long ldx, ldy;
+    int nseq, seq_len, ntok, C, silu;
+    // backward
+    const void *dy, *dcache_out;
+    void *dx, *dcache_in;
+    float* part;
+    long long lddy, lddx;
+};
+
+// Row j (0 oldest) of the cache that sequence [s0, e0) leaves: taken from its own
+// tokens, and for a sequence shorter than W - 1 from its old cache.
+template <typename T, int W>
+__device__ void tail_rows(const Args& a, long long i0, long long step) {
+    const T* x = static_cast<const T*>(a.x);
+    const T* in = static_cast<const T*>(a.cache_in);
+    T* out = static_cast<T*>(a.cache_out);
+    const long long total = (long long)a.nseq * a.C;
+    for (long long i = i0; i < total; i += step) {
+        const int n = int(i / a.C), c = int(i % a.C);
+        const int s0 = seq_begin(a.cu, a.seq_len, n), e0 = seq_begin(a.cu, a.seq_len, n + 1);
+        T r[W - 1];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            const int p = e0 - (W - 1) + j;
+            r[j] = p >= s0 ? x[(long long)p * a.ldx + c]
+                           : (in ? in[((size_t)n * (W - 1) + (W - 1 + p - s0)) * a.C + c] : from_f32<T>(0.f));
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) out[((size_t)n * (W - 1) + j) * a.C + c] = r[j];
+    }
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(256) tail_kernel(const Args a) {
+    tail_rows<T, W>(a, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
+}
+
+// The taps of a thread's channels: w[u][j], j = 0 the oldest.
+template <typename T, int W, int kE>
+__device__ __forceinline__ void load_taps(const T* w, int c0, float (&f)[kE][W]) {
+    if constexpr (kE > 1 && (W * sizeof(T)) % 8 == 0) {  // c0 is a multiple of kE: 16-byte aligned runs
+        constexpr int kP = int(16 / sizeof(T));
+#pragma unroll
+        for (int i = 0; i < kE * W / kP; ++i) {
+            float t[kP];
+            unpack16(reinterpret_cast<const uint4*>(w + (size_t)c0 * W)[i], t, T());
+#pragma unroll
+            for (int k = 0; k < kP; ++k) f[(i * kP + k) / W][(i * kP + k) % W] = t[k];
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < kE; ++u)
+#pragma unroll
+            for (int j = 0; j < W; ++j) f[u][j] = to_f32<T>(w[(size_t)(c0 + u) * W + j]);
+    }
+}
+
+// A block: 128 vectors of channels (blockIdx.y) by kTok tokens (blockIdx.x).  All
+// rows of the run are requested before the first is used.
+template <typename T, int W, bool kVec, int kTok>
+__global__ void __launch_bounds__(128) fwd_kernel(const Args a) {
+    constexpr int kE = Pack<T, kVec>::kN;
+    const int c0 = (blockIdx.y * 128 + threadIdx.x) * kE;
+    if (c0 >= a.C) return;
+    const T* x = static_cast<const T*>(a.x) + c0;
+    T* y = static_cast<T*>(a.y) + c0;
+    const T* in = static_cast<const T*>(a.cache_in);
+    const int t0 = blockIdx.x * kTok, t1 = min(a.ntok, t0 + kTok);
+    Raw<T, kVec> rows[kTok];
+#pragma unroll
+    for (int j = 0; j < kTok; ++j)
+        if (t0 + j < t1) rows[j].load(x + (long long)(t0 + j) * a.ldx);
+    float w[kE][W], b[kE];
+    load_taps<T, W, kE>(static_cast<const T*>(a.w), c0, w);
+#pragma unroll
+    for (int u = 0; u < kE; ++u) b[u] = a.bias ? a.bias[c0 + u] : 0.f;
+    int n = seq_of(a.cu, a.nseq, a.seq_len, t0);
+    int s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
+    float h[W - 1][kE];  // inputs at t-(W-1) .. t-1
+    auto history = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            const int p = t - (W - 1) + j;
+            Raw<T, kVec> r;
+            if (p >= s_beg) r.load(x + (long long)p * a.ldx);
+            else if (in) r.load(in + ((size_t)n * (W - 1) + (W - 1 + p - s_beg)) * a.C + c0);
+            else r.zero();
+            r.get(h[j]);
+        }
+    };
+    history(t0);
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+        const int t = t0 + i;
+        if (t >= t1) break;
+        if (t >= s_end) {  // a new sequence starts at t (empty ones are skipped)
+            while (t >= s_end && n + 1 < a.nseq) {
+                ++n;
+                s_beg = s_end;
+                s_end = seq_begin(a.cu, a.seq_len, n + 1);
+            }
+            history(t);
+        }
+        float v[kE], o[kE];
+        rows[i].get(v);
+#pragma unroll
+        for (int u = 0; u < kE; ++u) {
+            float s = b[u];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) s += w[u][j] * h[j][u];
+            s += w[u][W - 1] * v[u];
+            o[u] = a.silu ? __fdividef(s, 1.f + __expf(-s)) : s;
+#pragma unroll
+            for (int j = 0; j + 1 < W - 1; ++j) h[j][u] = h[j + 1][u];
+            h[W - 2][u] = v[u];
+        }
+        rows[i].set(o);
+        rows[i].store(y + (long long)t * a.ldy);
+    }
+}
+
+// d SiLU(s) / ds, finite for every finite s (sigmoid(s) (1 + s (1 - sigmoid(s)))).
+__device__ __forceinline__ float dsilu(float s) {
+    const float g = sigmoidf(s);
+    return g * (1.f + s * (1.f - g));
+}
+
+// Backward.  A thread slides over its run of kRun tokens and W - 1 more: ds of a
+// token is formed once its window is complete, and the token W - 1 back then has
+// its whole gradient.  The run's sums for dw and db stay in registers and are
+// written as partial sums [run][W + 1][C].
+template <typename T, int W, bool kVec>
+__global__ void __launch_bounds__(128) bwd_kernel(const Args a, int kRun) {
+    constexpr int kE = Pack<T, kVec>::kN;
+    const int c0 = (blockIdx.y * 128 + threadIdx.x) * kE;
+    if (c0 >= a.C) return;
+    const T* x = static_cast<const T*>(a.x) + c0;
+    const T* dy = static_cast<const T*>(a.dy) + c0;
+    T* dx = static_cast<T*>(a.dx) + c0;
+    const T* in = static_cast<const T*>(a.cache_in);
+    const T* dout = static_cast<const T*>(a.dcache_out);
+    const int t0 = blockIdx.x * kRun, t1 = min(a.ntok, t0 + kRun);
+    float w[kE][W], b[kE], aw[W][kE], ab[kE];
+    load_taps<T, W, kE>(static_cast<const T*>(a.w), c0, w);
+#pragma unroll
+    for (int u = 0; u < kE; ++u) {
+        b[u] = a.bias ? a.bias[c0 + u] : 0.f;
+        ab[u] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) aw[j][u] = 0.f;
+    }
+    int n = seq_of(a.cu, a.nseq, a.seq_len, t0);
+    int s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
+    float h[W - 1][kE];   // inputs at t-(W-1) .. t-1
+    float g[W - 1][kE];   // gradients of the inputs at t-(W-1) .. t-1, as far as they are known
+    auto history = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            const int p = t - (W - 1) + j;
+            Raw<T, kVec> r;
+            if (p >= s_beg) r.load(x + (long long)p * a.ldx);
+            else if (in) r.load(in + ((size_t)n * (W - 1) + (W - 1 + p - s_beg)) * a.C + c0);
+            else r.zero();
+            r.get(h[j]);
+#pragma unroll
+            for (int u = 0; u < kE; ++u) g[j][u] = 0.f;
+        }
+    };
+    // the gradient of input p of the current sequence is complete: add what flows back
+    // through the cache that the sequence leaves, and store it
+    auto finish = [&](int p, const float* v) {
+        if (p < s_beg || p < t0 || p >= t1) return;
+        float f[kE];
+#pragma unroll
+        for (int u = 0; u < kE; ++u) f[u] = v[u];
+        if (dout && p >= s_end - (W - 1)) {
+            Raw<T, kVec> r;
+            float e[kE];
+            r.load(dout + ((size_t)n * (W - 1) + (p - (s_end - (W - 1)))) * a.C + c0);
+            r.get(e);
+#pragma unroll
+            for (int u = 0; u < kE; ++u) f[u] += e[u];
+        }
+        Raw<T, kVec> r;
+        r.set(f);
+        r.store(dx + (long long)p * a.lddx);
+    };
+    history(t0);
+    const int t2 = min(a.ntok, t1 + W - 1);
+    Raw<T, kVec> nx, nd;  // the next token's rows, one step ahead
+    if (t0 < t2) {
+        nx.load(x + (long long)t0 * a.ldx);
+        nd.load(dy + (long long)t0 * a.lddy);
+    }
+    for (int t = t0; t < t2; ++t) {
+        if (t >= s_end) {
+            for (int j = 0; j < W - 1; ++j) finish(t - (W - 1) + j, g[j]);
+            if (t >= t1) {
+                s_end = t;  // nothing of this run is left
+                break;
+            }
+            while (t >= s_end && n + 1 < a.nseq) {
+                ++n;
+                s_beg = s_end;
+                s_end = seq_begin(a.cu, a.seq_len, n + 1);
+            }
+            history(t);
+        }
+        float v[kE], d[kE], dn[kE];
+        nx.get(v);
+        nd.get(d);
+        if (t + 1 < t2) {
+            nx.load(x + (long long)(t + 1) * a.ldx);
+            nd.load(dy + (long long)(t + 1) * a.lddy);
+        }
+        const bool mine = t < t1;  // the run's own tokens count for dw and db
+#pragma unroll
+        for (int u = 0; u < kE; ++u) {
+            if (a.silu) {
+                float s = b[u];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) s += w[u][j] * h[j][u];
+                s += w[u][W - 1] * v[u];
+                d[u] *= dsilu(s);
+            }
+            if (mine) {
+                ab[u] += d[u];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) aw[j][u] += d[u] * h[j][u];
+                aw[W - 1][u] += d[u] * v[u];
+            }
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) g[j][u] += w[u][j] * d[u];
+            dn[u] = w[u][W - 1] * d[u];
+        }
+        finish(t - (W - 1), g[0]);
+#pragma unroll
+        for (int u = 0; u < kE; ++u) {
+#pragma unroll
+            for (int j = 0; j + 1 < W - 1; ++j) {
+                h[j][u] = h[j + 1][u];
+                g[j][u] = g[j + 1][u];
+            }
+            h[W - 2][u] = v[u];
+            g[W - 2][u] = dn[u];
+        }
+    }
+    if (t2 == a.ntok && s_end >= t2)  // the axis ends here: the last inputs have no later token
+        for (int j = 0; j < W - 1; ++j) finish(t2 - (W - 1) + j, g[j]);
+    float* p = a.part + (size_t)blockIdx.x * (W + 1) * a.C + c0;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int u = 0; u < kE; ++u) p[(size_t)j * a.C + u] = aw[j][u];
+#pragma unroll
+    for (int u = 0; u < kE; ++u) p[(size_t)W * a.C + u] = ab[u];
+}
+
+// Gradient of the incoming cache: row r (position p = s0 - (W - 1) + r) fed the first
+// tokens of its sequence, and a sequence shorter than W - 1 passes rows on.
+template <typename T, int W>
+__global__ void __launch_bounds__(128) bwd_cache_kernel(const Args a) {
+    const int c = blockIdx.x * 128 + threadIdx.x;
+    if (c >= a.C) return;
+    const T *x = static_cast<const T*>(a.x) + c, *dy = static_cast<const T*>(a.dy) + c;
+    const T* in = static_cast<const T*>(a.cache_in);
+    const T* dout = static_cast<const T*>(a.dcache_out);
+    float w[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j] = to_f32<T>(static_cast<const T*>(a.w)[(size_t)c * W + j]);
+    const float b = a.bias ? a.bias[c] : 0.f;
+    for (int n = blockIdx.y; n < a.nseq; n += gridDim.y) {
+        const int s0 = seq_begin(a.cu, a.seq_len, n), e0 = seq_begin(a.cu, a.seq_len, n + 1);
+        float h[2 * W - 2], g[W - 1];  // inputs from position s0 - (W - 1) on; the cache's gradient
+#pragma unroll
+        for (int i = 0; i < 2 * W - 2; ++i) {
+            if (i < W - 1) {
+                h[i] = in ? to_f32<T>(in[((size_t)n * (W - 1) + i) * a.C + c]) : 0.f;
+                g[i < W - 1 ? i : 0] = 0.f;
+            } else {
+                h[i] = s0 + i - (W - 1) < e0 ? to_f32<T>(x[(long long)(s0 + i - (W - 1)) * a.ldx]) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {  // token s0 + k: its window is h[k .. k + W - 1]
+            if (s0 + k < e0) {
+                float d = to_f32<T>(dy[(long long)(s0 + k) * a.lddy]);
+                if (a.silu) {
+                    float s = b;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) s += w[j] * h[k + j];
+                    d *= dsilu(s);
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (k + j < W - 1) g[k + j] += w[j] * d;
+            }
+        }
+        if (dout) {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                const int p = e0 - (W - 1) + j;
+                if (p < s0) {
+                    const float e = to_f32<T>(dout[((size_t)n * (W - 1) + j) * a.C + c]);
+#pragma unroll
+                    for (int r = 0; r < W - 1; ++r)
+                        if (r == W - 1 + p - s0) g[r] += e;
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < W - 1; ++r)
+            static_cast<T*>(a.dcache_in)[((size_t)n * (W - 1) + r) * a.C + c] = from_f32<T>(g[r]);
+    }
+}
+
+// dw [C][W] and db [C] from the runs' partial sums [run][W + 1][C].
+template <typename T, int W>
+__global__ void __launch_bounds__(256) bwd_sum_kernel(const float* __restrict__ part, int parts, int C, T* __restrict__ dw,
+                                                      float* __restrict__ db) {
+    __shared__ float s[8][33];
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
+    const size_t stride = (size_t)(W + 1) * C;
+    float v0 = 0.f, v1 = 0.f;
+    if (c < C) {
+        int p = row;
+        for (; p + 8 < parts; p += 16) {
+            v0 += part[p * stride + (size_t)j * C + c];
+            v1 += part[(p + 8) * stride + (size_t)j * C + c];
+        }
+        if (p < parts) v0 += part[p * stride + (size_t)j * C + c];
+    }
+    s[row][lane] = v0 + v1;
+    __syncthreads();
+    if (row == 0 && c < C) {
+        float t = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) t += s[r][lane];
+        if (j < W) {
+            if (dw) dw[(size_t)c * W + j] = from_f32<T>(t);
+        } else if (db) {
+            db[c] = t;
+        }
+    }
+}
+
+// One token per sequence; the cache moves up one row in place.
+template <typename T, int W, bool kVec>
+__global__ void __launch_bounds__(128) step_kernel(const Args a, T* __restrict__ cache) {
+    constexpr int kE = Pack<T, kVec>::kN;
+    const int nvec = a.C / kE;
+    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
+    if (i >= (long long)a.nseq * nvec) return;
+    const int n = int(i / nvec), c0 = int(i % nvec) * kE;
+    Raw<T, kVec> h[W];
+    T* cn = cache + (size_t)n * (W - 1) * a.C + c0;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) h[j].load(cn + (size_t)j * a.C);
+    h[W - 1].load(static_cast<const T*>(a.x) + n * a.ldx + c0);
+    float w[kE][W], s[kE];
+    load_taps<T, W, kE>(static_cast<const T*>(a.w), c0, w);
+#pragma unroll
+    for (int u = 0; u < kE; ++u) s[u] = a.bias ? a.bias[c0 + u] : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        float v[kE];
+        h[j].get(v);
+#pragma unroll
+        for (int u = 0; u < kE; ++u) s[u] += w[u][j] * v[u];
+        if (j > 0) h[j].store(cn + (size_t)(j - 1) * a.C);
+    }
+    if (a.silu) {
+#pragma unroll
+        for (int u = 0; u < kE; ++u) s[u] = __fdividef(s[u], 1.f + __expf(-s[u]));
+    }
+    h[0].set(s);
+    h[0].store(static_cast<T*>(a.y) + n * a.ldy + c0);
+}
+
+constexpr int kFwdTok = 12;
+
+// Tokens of one thread in the backward pass: long runs write few partial sums
+// ((W + 1) x 4 bytes per channel and run), short ones fill the SMs.
+static int bwd_run(int ntok, int C, int kE) {
+    const long long lanes = cdiv(cdiv(C, kE), 128);
+    const long long want = cdiv((long long)ntok * lanes, (long long)device_sm_count() * 8);
+    return int(want < 16 ? 16 : (want > 128 ? 128 : want));
+}
+
+template <typename T, int W>
+int fwd(const Args& a, bool vec, cudaStream_t st) {
+    if (a.ntok > 0) {
+        const int kE = vec ? int(16 / sizeof(T)) : 1;
+        const dim3 grid(unsigned(cdiv(a.ntok, kFwdTok)), unsigned(cdiv(cdiv(a.C, kE), 128)));
+        if (vec) fwd_kernel<T, W, true, kFwdTok><<<grid, 128, 0, st>>>(a);
+        else fwd_kernel<T, W, false, kFwdTok><<<grid, 128, 0, st>>>(a);
+    }
+    if (a.cache_out) {  // after the main kernel on the stream, so cache_out may be cache_in
+        const long long n = cdiv((long long)a.nseq * a.C, 256);
+        tail_kernel<T, W><<<unsigned(n < 4096 ? n : 4096), 256, 0, st>>>(a);
+    }
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+template <typename T, int W>
+int bwd(const Args& a, bool vec, void* dw, float* db, cudaStream_t st) {
+    const int kE = vec ? int(16 / sizeof(T)) : 1;
+    int parts = 0;
+    if (a.ntok > 0) {
+        const int run = bwd_run(a.ntok, a.C, kE);
+        parts = int(cdiv(a.ntok, run));
+        const dim3 grid(parts, unsigned(cdiv(cdiv(a.C, kE), 128)));
+        if (vec) bwd_kernel<T, W, true><<<grid, 128, 0, st>>>(a, run);
+        else bwd_kernel<T, W, false><<<grid, 128, 0, st>>>(a, run);
+    }
+    if (dw || db)
+        bwd_sum_kernel<T, W><<<dim3(unsigned(cdiv(a.C, 32)), W + 1), 256, 0, st>>>(a.part, parts, a.C,
+                                                                                   static_cast<T*>(dw), db);
+    if (a.dcache_in)
+        bwd_cache_kernel<T, W><<<dim3(unsigned(cdiv(a.C, 128)), a.nseq < 65535 ? a.nseq : 65535), 128, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+template <typename T, int W>
+int step(const Args& a, bool vec, void* cache, cudaStream_t st) {
+    const int kE = vec ? int(16 / sizeof(T)) : 1;
+    const unsigned grid = unsigned(cdiv((long long)a.nseq * (a.C / kE), 128));
+    if (vec) step_kernel<T, W, true><<<grid, 128, 0, st>>>(a, static_cast<T*>(cache));
+    else step_kernel<T, W, false><<<grid, 128, 0, st>>>(a, static_cast<T*>(cache));
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace conv
+
+size_t short_conv_bwd_workspace_bytes(int ntok, int C, int W) {
+    // the shortest runs of any element type and alignment
+    size_t parts = 0;
+    for (int e = 1; e <= 8; e *= 2) {
+        const size_t p = size_t(mix::cdiv(ntok, conv::bwd_run(ntok, C, e)));
+        if (p > parts) parts = p;
+    }
+    return mix::up256(parts * (W + 1) * C * sizeof(float));
+}
+
+// 16-byte vectors of channels: every row of every tensor starts on a 16-byte boundary.
+bool short_conv_vec(int C, int dtype, const void* const* ptrs, int np, const long long* lds, int nl) {
+    const int es = dtype == KDA_BF16 ? 2 : 4;
+    if ((long long)C * es % 16) return false;
+    for (int i = 0; i < np; ++i)
+        if (!mix::al16(ptrs[i])) return false;
+    for (int i = 0; i < nl; ++i)
+        if (lds[i] * es % 16) return false;
+    return true;
+}
+
+#define KDA_CONV_DISPATCH(CALL)                                     \
+    if (dtype == KDA_BF16) {                                        \
+        using T = __nv_bfloat16;                                    \
+        if (W == 2) { constexpr int kW = 2; return CALL; }          \
+        if (W == 3) { constexpr int kW = 3; return CALL; }          \
+        constexpr int kW = 4;                                       \
+        return CALL;                                                \
+    }                                                               \
+    using T = float;                                                \
+    if (W == 2) { constexpr int kW = 2; return CALL; }              \
+    if (W == 3) { constexpr int kW = 3; return CALL; }              \
+    constexpr int kW = 4;                                           \
+    return CALL;
+
+int launch_short_conv_fwd(const void* x, long long ldx, const void* w, const float* bias, void* y, long long ldy,
+                          const void* cache_in, void* cache_out, const int32_t* cu, int nseq, int seq_len, int ntok,
+                          int C, int W, int dtype, int silu, cudaStream_t st) {
+    conv::Args a{};
+    a.x = x; a.ldx = ldx; a.w = w; a.bias = bias; a.y = y; a.ldy = ldy;
+    a.cache_in = cache_in; a.cache_out = cache_out;
+    a.cu = cu; a.nseq = nseq; a.seq_len = seq_len; a.ntok = ntok; a.C = C; a.silu = silu;
+    const void* ptrs[] = {x, w, y, cache_in, cache_out};
+    const long long lds[] = {ldx, ldy};
+    const bool vec = short_conv_vec(C, dtype, ptrs, 5, lds, 2);
+    KDA_CONV_DISPATCH((conv::fwd<T, kW>(a, vec, st)))
+}
+
+int launch_short_conv_bwd(const void* dy, long long lddy, const void* x, long long ldx, const void* w,
+                          const float* bias, const void* cache_in, const void* dcache_out, void* dx, long long lddx,
+                          void* dw, float* db, void* dcache_in, const int32_t* cu, int nseq, int seq_len, int ntok,
+                          int C, int W, int dtype, int silu, void* ws, cudaStream_t st) {
+    conv::Args a{};
+    a.x = x; a.ldx = ldx; a.w = w; a.bias = bias;
+    a.cache_in = cache_in; a.dcache_out = dcache_out; a.dcache_in = dcache_in;
+    a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
+    a.part = static_cast<float*>(ws);
+    a.cu = cu; a.nseq = nseq; a.seq_len = seq_len; a.ntok = ntok; a.C = C; a.silu = silu;
+    const void* ptrs[] = {x, w, dy, dx, cache_in, dcache_out};
+    const long long lds[] = {ldx, lddy, lddx};
+    const bool vec = short_conv_vec(C, dtype, ptrs, 6, lds, 3);
+    KDA_CONV_DISPATCH((conv::bwd<T, kW>(a, vec, dw, db, st)))
+}
+
+int launch_short_conv_step(const void* x, long long ldx, const void* w, const float* bias, void* cache, void* y,
+                           long long ldy, int B, int C, int W, int dtype, int silu, cudaStream_t st) {
+    conv::Args a{};
+    a.x = x; a.ldx = ldx; a.w = w; a.bias = bias; a.y = y; a.ldy = ldy;
+    a.nseq = B; a.seq_len = 1; a.ntok = B; a.C = C; a.silu = silu;
+    const void* ptrs[] = {x, w, y, cache};
+    const long long lds[] = {ldx, ldy};
+    const bool vec = short_conv_vec(C, dtype, ptrs, 4, lds, 2);
+    KDA_CONV_DISPATCH((conv::step<T, kW>(a, vec, cache, st)))
+}
+
+}  // namespace kda

@@ -1,0 +1,548 @@
+// The projection GEMM with a bias, an activation and a residual in its epilogue,
+// and its gradients, on sm_100a.
+//
+//   s = x W^T + b,  y = act(s) + residual          x [M, K], W [N, K], y [M, N]
+//   ds = dy act'(s):  dx = ds W,  dW = ds^T x,  db = sum over rows of ds
+//
+// "Kimi Linear: An Expressive, Efficient Attention Architecture", section "Neural
+// Parameterization", has bias-free projections (kda_linear_bf16); the mixers next
+// to them have a bias, an activation or a residual after theirs, and training
+// needs the gradients.  All three products run in one persistent tcgen05 kernel
+// with the roles of kda_gemm.cu (a TMA producer warp, one MMA-issuing thread, two
+// accumulators in TMEM, eight epilogue warps).  What differs by product is which
+// axis of an operand is contiguous: x and W of the forward pass hold the summed
+// axis contiguous (K-major tiles); in dx = ds W the summed axis is the row index
+// of W, in dW = ds^T x it is the row index of both, so those tiles are loaded as
+// 64-column by 64-row boxes and read as MN-major operands.  No operand is ever
+// transposed in memory.  bf16 operands, fp32 accumulation; ds is rounded to bf16
+// because it is an operand of two tensor-core products.
+#include "kda_gemm.cuh"
+#include "kda_mixer.cuh"
+
+namespace kda {
+namespace lin {
+
+using namespace gemm;  // the GEMM's TMA, TMEM and staging helpers, and its tile BM x BK
+
+enum Act { kNone = KDA_ACT_NONE, kRelu = KDA_ACT_RELU, kGelu = KDA_ACT_GELU, kSilu = KDA_ACT_SILU,
+           kSoftplus = KDA_ACT_SOFTPLUS };
+
+template <int kBN, bool kPre>
+struct LPlan {
+    static constexpr uint32_t kB = kBN * BK * 2, kStage = kABytes + kB;
+    static constexpr uint32_t kStagingBytes = kPre ? 8192 : 4096;  // per epilogue warp: a tile of y, one of s
+    // as many stages as fit beside the staging tiles and the barriers, at most 8
+    static constexpr int kFit = int((232448 - 1280 - kEpiWarps * kStagingBytes) / kStage);
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
+    static constexpr uint32_t OFF_STAGING = kStages * kStage;
+    static constexpr uint32_t OFF_BARS = OFF_STAGING + kEpiWarps * kStagingBytes;
+    static constexpr uint32_t kSmem = OFF_BARS + 256 + 1024;
+    static_assert(kStages >= 3 && kSmem <= 232448, "shared-memory plan");
+};
+
+struct LArgs {
+    int M, N, K, tiles_m, tiles_n;
+    const float* bias;
+    const __nv_bfloat16* res;
+    int ldr, res_vec, act;
+    __nv_bfloat16 *c, *pre;  // outputs, for the columns that no TMA store writes
+    int ldc, ldp;
+};
+
+// A TMA store clips a row at whole 16-byte groups, so it would write past an N that is
+// not a multiple of 8: the maps of the outputs end at the last whole group, and the
+// N % 8 columns after it are stored by each row's thread.
+template <int kN>
+__device__ __forceinline__ void store_ragged(__nv_bfloat16* row, const float* v, int first, int cols) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+        if (j >= first && j < cols) row[j] = __float2bfloat16_rn(v[j]);
+}
+
+__device__ __forceinline__ float gelu(float x) { return 0.5f * x * (1.f + erff(x * 0.70710678118654752f)); }
+// softplus with the fast log: the result is rounded to bf16.  Below -8 the sum 1 + e^x
+// keeps too few bits of e^x, and log(1 + e^x) is e^x to within e^x / 2 < 2^-12 of it.
+__device__ __forceinline__ float softplus_bf16(float x) {
+    const float e = __expf(-fabsf(x));
+    return fmaxf(x, 0.f) + (e < 3.3e-4f ? e : __logf(1.f + e));
+}
+
+template <int kN>
+__device__ __forceinline__ void apply_act(float* v, int act) {
+    switch (act) {
+        case kRelu:
+#pragma unroll
+            for (int j = 0; j < kN; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];  // keeps NaN
+            break;
+        case kGelu:
+#pragma unroll
+            for (int j = 0; j < kN; ++j) v[j] = gelu(v[j]);
+            break;
+        case kSilu:
+#pragma unroll
+            for (int j = 0; j < kN; ++j) v[j] = __fdividef(v[j], 1.f + __expf(-v[j]));
+            break;
+        case kSoftplus:
+#pragma unroll
+            for (int j = 0; j < kN; ++j) v[j] = softplus_bf16(v[j]);
+            break;
+        default: break;
+    }
+}
+
+template <int kBN, bool kAMN, bool kBMN, bool kPre>
+__global__ void __launch_bounds__(gemm::kThreads, 1)
+    kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+           const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_p, const LArgs p) {
+    using P = LPlan<kBN, kPre>;
+    constexpr int kStages = P::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(sm);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + P::OFF_BARS);
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint32_t* sTmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    volatile int* sAbort = reinterpret_cast<volatile int*>(sTmem + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int total = p.tiles_m * p.tiles_n;
+    const int nkb = (p.K + BK - 1) / BK;
+
+    if (warp == 0) {
+        tmem_alloc(sTmem, 2 * kBN);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], kEpiWarps);
+        }
+        *sAbort = 0;
+        fence_mbar_init();
+    }
+    if (tid == 64) {
+        prefetch_tmap(&map_a);
+        prefetch_tmap(&map_b);
+        prefetch_tmap(&map_c);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *sTmem;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            int stage = 0, issued = 0;  // issued: loads whose full barrier may still be pending at exit
+            uint32_t phase = 0;
+            for (int t = blockIdx.x; t < total && !*sAbort; t += gridDim.x) {
+                const int m0 = (t / p.tiles_n) * BM, n0 = (t % p.tiles_n) * kBN;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1, 8)) {
+                        *sAbort = 1;
+                        break;
+                    }
+                    uint8_t* sa = sm + stage * P::kStage;
+                    uint8_t* sb = sa + kABytes;
+                    mbar_arrive_expect_tx(&full[stage], P::kStage);
+                    if constexpr (kAMN) {
+#pragma unroll
+                        for (int i = 0; i < BM / 64; ++i) tma_load_2d(sa + i * 8192, &map_a, &full[stage], m0 + 64 * i, kb * BK);
+                    } else {
+                        tma_load_2d(sa, &map_a, &full[stage], kb * BK, m0);
+                    }
+                    if constexpr (kBMN) {
+#pragma unroll
+                        for (int i = 0; i < kBN / 64; ++i) tma_load_2d(sb + i * 8192, &map_b, &full[stage], n0 + 64 * i, kb * BK);
+                    } else {
+                        tma_load_2d(sb, &map_b, &full[stage], kb * BK, n0);
+                    }
+                    ++issued;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (*sAbort) {  // let every load this thread issued land before the CTA exits
+                for (int s = 0; s < kStages && issued > 0; ++s, --issued) {
+                    if (--stage < 0) {
+                        stage = kStages - 1;
+                        phase ^= 1;
+                    }
+                    mbar_wait(&full[stage], phase, 9);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            int stage = 0, i = 0;
+            uint32_t phase = 0;
+            bool pending = false;  // a commit whose barrier may not have arrived yet
+            for (int t = blockIdx.x; t < total && !*sAbort; t += gridDim.x, ++i) {
+                const int buf = i & 1;
+                const uint32_t aph = (i >> 1) & 1;
+                int nw = p.N - (t % p.tiles_n) * kBN;
+                nw = nw >= kBN ? kBN : ((nw + 15) & ~15);
+                const uint32_t idesc = idesc_bf16(BM, nw, kAMN, kBMN);
+                if (!mbar_wait(&acc_empty[buf], aph ^ 1, 10)) {
+                    *sAbort = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t dtm = tbase + uint32_t(buf * kBN);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait(&full[stage], phase, 11)) {
+                        *sAbort = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = sbase + stage * P::kStage, sb = sa + kABytes;
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k) {
+                        const uint64_t da = kAMN ? sdesc_sw128(sa + k * 2048, 8192, 1024) : sdesc_sw128(sa + k * 32, 16, 1024);
+                        const uint64_t db = kBMN ? sdesc_sw128(sb + k * 2048, 8192, 1024) : sdesc_sw128(sb + k * 32, 16, 1024);
+                        umma_bf16(dtm, da, db, idesc, (kb | k) != 0);
+                    }
+                    umma_commit(&empty[stage]);
+                    pending = true;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (*sAbort) break;
+                umma_commit(&acc_full[buf]);
+            }
+            if (*sAbort && pending) {  // the last MMAs still read shared memory: let them finish
+                const int last = (stage + kStages - 1) % kStages;
+                mbar_wait(&empty[last], stage == 0 ? phase ^ 1 : phase, 12);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        const int ew = warp - 2;
+        const int quad = warp & 3;   // TMEM lane quadrant this warp may read
+        const int half = ew >> 2;    // column half of the tile (a 64-wide tile has one)
+        constexpr int kChunks = kBN >= 128 ? kBN / 128 : 1;
+        const uint32_t stg = sbase + P::OFF_STAGING + uint32_t(ew) * P::kStagingBytes;
+        uint8_t* stg_p = sm + P::OFF_STAGING + ew * P::kStagingBytes;
+        int i = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x, ++i) {
+            const int buf = i & 1;
+            const uint32_t aph = (i >> 1) & 1;
+            const int m0 = (t / p.tiles_n) * BM, n0 = (t % p.tiles_n) * kBN;
+            const int row = m0 + quad * 32 + lane;  // output row of this thread
+            const int cols = min(kBN, p.N - n0);    // valid columns of this tile
+            // this thread's 64 residual values of a chunk, requested before the accumulator
+            // is waited for: 128 contiguous bytes of its row
+            uint4 res[8];
+            auto load_res = [&](int c0) {
+                if (p.res && row < p.M && p.res_vec) {
+                    const __nv_bfloat16* r = p.res + (size_t)row * p.ldr + n0 + c0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (c0 + 8 * j + 8 <= cols) res[j] = __ldg(reinterpret_cast<const uint4*>(r) + j);
+                }
+            };
+            const int h0 = kBN >= 128 ? half * (kBN / 2) : 0;
+            if (h0 < cols) load_res(h0);
+            const bool ok = mbar_wait(&acc_full[buf], aph, 13);
+            if (__any_sync(0xffffffffu, !ok) || *sAbort) {
+                *sAbort = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t tacc = tbase + uint32_t(buf * kBN) + (uint32_t(quad * 32) << 16);
+#pragma unroll 1
+            for (int ch = 0; ch < kChunks; ++ch) {
+                const int c0 = h0 + ch * 64;  // tile column of this 64-wide chunk
+                if (c0 >= cols || (kBN < 128 && half)) break;
+                float v[64];
+                tmem_ld32(tacc + c0, v);
+                tmem_ld32(tacc + c0 + 32, v + 32);
+                tmem_wait_ld();
+                if (p.bias) {
+                    const float* b = p.bias + n0 + c0;
+                    if (c0 + 64 <= cols && (reinterpret_cast<uintptr_t>(b) & 15) == 0) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float4 q = __ldg(reinterpret_cast<const float4*>(b) + j);
+                            v[4 * j] += q.x;
+                            v[4 * j + 1] += q.y;
+                            v[4 * j + 2] += q.z;
+                            v[4 * j + 3] += q.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (c0 + j < cols) v[j] += __ldg(b + j);
+                    }
+                }
+                if (lane == 0) gemm::bulk_wait_read0();  // the previous stores have read the staging tiles
+                __syncwarp();
+                const int whole = (p.N & ~7) - (n0 + c0);  // chunk columns that the TMA store covers
+                const bool ragged = whole < 64 && (p.N & 7) && row < p.M;
+                uint32_t w32[32];
+                if constexpr (kPre) {
+                    if (ragged) store_ragged<64>(p.pre + (size_t)row * p.ldp + n0 + c0, v, whole, cols - c0);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) w32[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
+                    stage_row(stg + 4096, lane, w32);
+                }
+                apply_act<64>(v, p.act);
+                if (p.res && row < p.M) {
+                    if (p.res_vec) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (c0 + 8 * j + 8 <= cols) {
+                                float f[8];
+                                mix::unpack16(res[j], f, __nv_bfloat16());
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) v[8 * j + u] += f[u];
+                            } else {
+#pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    if (c0 + 8 * j + u < cols)
+                                        v[8 * j + u] += __bfloat162float(p.res[(size_t)row * p.ldr + n0 + c0 + 8 * j + u]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (c0 + j < cols) v[j] += __bfloat162float(p.res[(size_t)row * p.ldr + n0 + c0 + j]);
+                    }
+                }
+                if (ch + 1 < kChunks && c0 + 64 < cols) load_res(c0 + 64);
+                if (ragged) store_ragged<64>(p.c + (size_t)row * p.ldc + n0 + c0, v, whole, cols - c0);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) w32[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
+                stage_row(stg, lane, w32);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && whole > 0) {
+                    tma_store_2d(&map_c, stg_p, n0 + c0, m0 + quad * 32);
+                    if (kPre) tma_store_2d(&map_p, stg_p + 4096, n0 + c0, m0 + quad * 32);
+                    gemm::bulk_commit();
+                }
+            }
+            // this warp has read its part of the accumulator: hand it back to the MMA warp
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        }
+        if (lane == 0) gemm::bulk_wait0();  // every store of this warp has completed
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tbase, 2 * kBN);
+}
+
+// C [M, N] = A B^T summed over K.  K-major operands: A [M, K], B [N, K]; MN-major
+// ones hold the summed axis as rows: A [K, M], B [K, N].
+template <int kBN, bool kAMN, bool kBMN, bool kPre>
+static int launch_tile(const void* A, int lda, const void* B, int ldb, void* C, int ldc, void* pre, int ldp, LArgs a,
+                       cudaStream_t st, const char** why) {
+    CUtensorMap ma, mb, mc, mp;
+    const bool ok = (kAMN ? map_2d(&ma, A, false, a.K, a.M, lda, 64, BK) : map_2d(&ma, A, false, a.M, a.K, lda, BK, BM)) &&
+                    (kBMN ? map_2d(&mb, B, false, a.K, a.N, ldb, 64, BK) : map_2d(&mb, B, false, a.N, a.K, ldb, BK, kBN)) &&
+                    map_2d(&mc, C, false, a.M, a.N < 8 ? 8 : a.N & ~7, ldc, 64, 32) &&
+                    (kPre ? map_2d(&mp, pre, false, a.M, a.N < 8 ? 8 : a.N & ~7, ldp, 64, 32) : (mp = mc, true));
+    if (!ok) {
+        *why = "cuTensorMapEncodeTiled failed for a GEMM operand";
+        return KDA_ERR_CUDA;
+    }
+    a.c = static_cast<__nv_bfloat16*>(C);
+    a.ldc = ldc;
+    a.pre = static_cast<__nv_bfloat16*>(pre);
+    a.ldp = ldp;
+    a.tiles_m = (a.M + BM - 1) / BM;
+    a.tiles_n = (a.N + kBN - 1) / kBN;
+    const long long tiles = (long long)a.tiles_m * a.tiles_n;
+    const int sms = device_sm_count(), grid = int(tiles < sms ? tiles : sms);
+    auto kern = kernel<kBN, kAMN, kBMN, kPre>;
+    constexpr uint32_t smem = LPlan<kBN, kPre>::kSmem;
+    if (!set_smem_attr(kern, smem)) {
+        *why = "cudaFuncSetAttribute failed for the GEMM kernel";
+        return KDA_ERR_CUDA;
+    }
+    kern<<<grid, gemm::kThreads, smem, st>>>(ma, mb, mc, mp, a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        *why = cudaGetErrorString(e);
+        return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
+}
+
+template <bool kAMN, bool kBMN, bool kPre>
+static int launch(const void* A, int lda, const void* B, int ldb, void* C, int ldc, void* pre, int ldp, const LArgs& a,
+                  cudaStream_t st, const char** why) {
+    return launch_tile<256, kAMN, kBMN, kPre>(A, lda, B, ldb, C, ldc, pre, ldp, a, st, why);
+}
+
+__device__ __forceinline__ float dact(float x, int act) {
+    switch (act) {
+        case kRelu: return x > 0.f ? 1.f : 0.f;
+        case kGelu:
+            return 0.5f * (1.f + erff(x * 0.70710678118654752f)) + x * 0.39894228040143268f * __expf(-0.5f * x * x);
+        case kSilu: {
+            const float g = mix::sigmoidf(x);
+            return g * (1.f + x * (1.f - g));
+        }
+        case kSoftplus: return mix::sigmoidf(x);
+        default: return 1.f;
+    }
+}
+
+// ds = dy act'(s) in bf16 (when ds is not NULL) and its column sums over a run of
+// rows, part[blockIdx.y][N], summed from the unrounded values.  A block: 32 vectors
+// of 8 columns by 8 rows.  Bound by HBM.
+template <bool kVec>
+__global__ void __launch_bounds__(256)
+    act_grad_kernel(const __nv_bfloat16* __restrict__ dy, long long lddy, const __nv_bfloat16* __restrict__ s,
+                    long long lds, __nv_bfloat16* __restrict__ ds, long long ldds, float* __restrict__ part, int M, int N,
+                    int rows_per_block, int act) {
+    using V = mix::Raw<__nv_bfloat16, kVec>;
+    constexpr int kE = kVec ? 8 : 1;
+    __shared__ float red[8][32 * kE + 1];
+    const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int c0 = (blockIdx.x * 32 + lane) * kE;
+    const long long r0 = (long long)blockIdx.y * rows_per_block;
+    const long long r1 = r0 + rows_per_block < M ? r0 + rows_per_block : M;
+    float sum[kE];
+#pragma unroll
+    for (int u = 0; u < kE; ++u) sum[u] = 0.f;
+    if (c0 < N) {
+#pragma unroll 4
+        for (long long r = r0 + ty; r < r1; r += 8) {
+            V vd, vs;
+            float d[kE], x[kE];
+            vd.load(dy + r * lddy + c0);
+            if (act != kNone) vs.load(s + r * lds + c0);
+            vd.get(d);
+            if (act != kNone) {
+                vs.get(x);
+#pragma unroll
+                for (int u = 0; u < kE; ++u) d[u] *= dact(x[u], act);
+            }
+#pragma unroll
+            for (int u = 0; u < kE; ++u) sum[u] += d[u];
+            if (ds) {
+                vd.set(d);
+                vd.store(ds + r * ldds + c0);
+            }
+        }
+    }
+    if (!part) return;
+#pragma unroll
+    for (int u = 0; u < kE; ++u) red[ty][u * 32 + lane] = sum[u];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * kE; i += 256) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += red[k][i];
+        const int c = (blockIdx.x * 32 + (i & 31)) * kE + (i >> 5);
+        if (c < N) part[(size_t)blockIdx.y * N + c] = t;
+    }
+}
+
+// Rows per block of act_grad_kernel: a multiple of 8 that gives about four blocks an SM.
+static int grad_rows(int M, int N, int kE) {
+    const long long cols = mix::cdiv(N, 32 * kE);
+    const long long want = mix::cdiv((long long)M * cols, (long long)device_sm_count() * 4);
+    const long long r = mix::cdiv(want, 8) * 8;
+    return int(r < 32 ? 32 : r);
+}
+
+}  // namespace lin
+
+int launch_linear_act(const void* x, int ldx, const void* W, int ldw, const float* bias, const void* res, int ldr,
+                      void* y, int ldy, void* pre, int ldp, int M, int N, int K, int act, cudaStream_t st,
+                      const char** why) {
+    lin::LArgs a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.bias = bias;
+    a.res = static_cast<const __nv_bfloat16*>(res);
+    a.ldr = ldr;
+    a.res_vec = res && mix::al16(res) && ldr % 8 == 0;
+    a.act = act;
+    if (pre) return lin::launch<false, false, true>(x, ldx, W, ldw, y, ldy, pre, ldp, a, st, why);
+    return lin::launch<false, false, false>(x, ldx, W, ldw, y, ldy, nullptr, 0, a, st, why);
+}
+
+struct LinearBwdPlan {
+    int ldds;
+    size_t off_part, total;
+};
+static LinearBwdPlan linear_bwd_plan(int M, int N) {
+    LinearBwdPlan p{};
+    p.ldds = (N + 7) & ~7;
+    p.off_part = mix::up256(size_t(M) * p.ldds * 2);
+    size_t parts = 0;  // the more blocks of either vector width
+    for (int e = 1; e <= 8; e += 7) {
+        const size_t n = size_t(mix::cdiv(M, lin::grad_rows(M, N, e)));
+        if (n > parts) parts = n;
+    }
+    p.total = p.off_part + mix::up256(parts * N * sizeof(float));
+    return p;
+}
+size_t linear_act_bwd_workspace_bytes(int M, int N) { return linear_bwd_plan(M, N).total; }
+
+int launch_linear_act_bwd(const void* dy, int lddy, const void* x, int ldx, const void* W, int ldw, const void* pre,
+                          int ldp, void* dx, int lddx, void* dW, int lddw, float* dbias, int M, int N, int K, int act,
+                          void* ws, cudaStream_t st, const char** why) {
+    using bf16 = __nv_bfloat16;
+    const LinearBwdPlan pl = linear_bwd_plan(M, N);
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    // dy itself is the operand when there is no activation and TMA can read it
+    const bool direct = act == KDA_ACT_NONE && mix::al16(dy) && lddy % 8 == 0;
+    bf16* ds = direct ? nullptr : reinterpret_cast<bf16*>(b);
+    float* part = dbias ? reinterpret_cast<float*>(b + pl.off_part) : nullptr;
+    const bool vec = N % 8 == 0 && mix::al16(dy) && lddy % 8 == 0 && (!pre || (mix::al16(pre) && ldp % 8 == 0));
+    if (ds || part) {
+        const int kE = vec ? 8 : 1, rows = lin::grad_rows(M, N, kE);
+        const int parts = int(mix::cdiv(M, rows));
+        const dim3 grid(unsigned(mix::cdiv(N, 32 * kE)), parts);
+        const bf16 *d = static_cast<const bf16*>(dy), *s = static_cast<const bf16*>(pre);
+        if (vec) lin::act_grad_kernel<true><<<grid, 256, 0, st>>>(d, lddy, s, ldp, ds, pl.ldds, part, M, N, rows, act);
+        else lin::act_grad_kernel<false><<<grid, 256, 0, st>>>(d, lddy, s, ldp, ds, pl.ldds, part, M, N, rows, act);
+        if (part)
+            mix::sum_parts_kernel<float><<<unsigned(mix::cdiv(N, 32)), 256, 0, st>>>(part, parts, N, dbias, N);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) {
+            *why = cudaGetErrorString(e);
+            return KDA_ERR_CUDA;
+        }
+    }
+    const void* op = direct ? dy : ds;
+    const int ldop = direct ? lddy : pl.ldds;
+    lin::LArgs a{};
+    if (dx) {  // [M, K] = ds [M, N] W [N, K]
+        a.M = M;
+        a.N = K;
+        a.K = N;
+        const int rc = lin::launch<false, true, false>(op, ldop, W, ldw, dx, lddx, nullptr, 0, a, st, why);
+        if (rc != KDA_OK) return rc;
+    }
+    if (dW) {  // [N, K] = ds^T [N, M] x [M, K]
+        a.M = N;
+        a.N = K;
+        a.K = M;
+        const int rc = lin::launch<true, true, false>(op, ldop, x, ldx, dW, lddw, nullptr, 0, a, st, why);
+        if (rc != KDA_OK) return rc;
+    }
+    return KDA_OK;
+}
+
+}  // namespace kda

@@ -1,0 +1,397 @@
+// Layer norm over the last axis, forward and backward.
+//
+//   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps), y = (x - mu) r w + b
+//   with xh = (x - mu) r and c = w dy:
+//   dx = r (c - mean(c) - xh mean(c xh)),  dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// Both passes are bound by HBM: forward reads x and writes y, backward reads dy
+// and x and writes dx.  A row therefore stays in registers from its load to its
+// store (mean first, then the centred squares, so no cancellation), in 16-byte
+// vectors held by one warp or by one block; widths that do not divide into
+// 16-byte vectors, unaligned rows and rows beyond a block's registers take a
+// kernel that walks the row again from the caches.  Statistics and sums are fp32.
+#include "kda_mixer.cuh"
+
+namespace kda {
+namespace norm {
+
+using namespace mix;
+
+template <int kTpr>
+__device__ __forceinline__ float row_sum(float v, float* sred) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (kTpr > 32) {
+        constexpr int kW = kTpr / 32;
+        if ((threadIdx.x & 31) == 0) sred[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) v += sred[w];
+    }
+    return v;
+}
+
+// kTpr threads hold one row, kVpt vectors each; a block of max(kTpr, 128) threads.
+template <typename T, int kTpr, int kVpt>
+__global__ void __launch_bounds__(kTpr > 128 ? kTpr : 128)
+    fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ b,
+               T* __restrict__ y, long long ldy, float* __restrict__ mean, float* __restrict__ rstd, int M, int N,
+               float eps) {
+    constexpr int kE = Pack<T, true>::kN, kRows = kTpr > 128 ? 1 : 128 / kTpr;
+    __shared__ float sred[2][kTpr > 32 ? kTpr / 32 : 1];
+    const int t = threadIdx.x % kTpr;
+    const long long row = (long long)blockIdx.x * kRows + threadIdx.x / kTpr;
+    if (kTpr == 32 && row >= M) return;  // whole warps; with one row per block the grid is exact
+    const T* xr = x + row * ldx;
+    Raw<T, true> raw[kVpt];
+    const int nvec = N / kE;
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i) {
+        const int j = t + i * kTpr;
+        if (j < nvec) raw[i].load(xr + (size_t)j * kE);
+        else raw[i].zero();
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i) {
+        float f[kE];
+        raw[i].get(f);
+#pragma unroll
+        for (int u = 0; u < kE; ++u) s += f[u];
+    }
+    const float mu = row_sum<kTpr>(s, sred[0]) / float(N);
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i) {
+        if (t + i * kTpr >= nvec) break;
+        float f[kE];
+        raw[i].get(f);
+#pragma unroll
+        for (int u = 0; u < kE; ++u) s += (f[u] - mu) * (f[u] - mu);
+    }
+    const float r = 1.f / sqrtf(row_sum<kTpr>(s, sred[1]) / float(N) + eps);
+    if (t == 0) {
+        if (mean) mean[row] = mu;
+        if (rstd) rstd[row] = r;
+    }
+    T* yr = y + row * ldy;
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i) {
+        const int j = t + i * kTpr;
+        if (j >= nvec) break;
+        float f[kE];
+        raw[i].get(f);
+#pragma unroll
+        for (int u = 0; u < kE; u += 4) {
+            const float4 ww = w ? *reinterpret_cast<const float4*>(w + (size_t)j * kE + u) : make_float4(1, 1, 1, 1);
+            const float4 bb = b ? *reinterpret_cast<const float4*>(b + (size_t)j * kE + u) : make_float4(0, 0, 0, 0);
+            f[u] = (f[u] - mu) * r * ww.x + bb.x;
+            f[u + 1] = (f[u + 1] - mu) * r * ww.y + bb.y;
+            f[u + 2] = (f[u + 2] - mu) * r * ww.z + bb.z;
+            f[u + 3] = (f[u + 3] - mu) * r * ww.w + bb.w;
+        }
+        raw[i].set(f);
+        raw[i].store(yr + (size_t)j * kE);
+    }
+}
+
+// Any width and alignment: one block per row, element by element; the second and
+// third walk over the row hit the caches.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    fwd_any_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ b,
+                   T* __restrict__ y, long long ldy, float* __restrict__ mean, float* __restrict__ rstd, int N,
+                   float eps) {
+    __shared__ float sred[2][8];
+    const long long row = blockIdx.x;
+    const T* xr = x + row * ldx;
+    float s = 0.f;
+    for (int j = threadIdx.x; j < N; j += 256) s += to_f32<T>(xr[j]);
+    const float mu = row_sum<256>(s, sred[0]) / float(N);
+    s = 0.f;
+    for (int j = threadIdx.x; j < N; j += 256) {
+        const float d = to_f32<T>(xr[j]) - mu;
+        s += d * d;
+    }
+    const float r = 1.f / sqrtf(row_sum<256>(s, sred[1]) / float(N) + eps);
+    if (threadIdx.x == 0) {
+        if (mean) mean[row] = mu;
+        if (rstd) rstd[row] = r;
+    }
+    T* yr = y + row * ldy;
+    for (int j = threadIdx.x; j < N; j += 256)
+        yr[j] = from_f32<T>((to_f32<T>(xr[j]) - mu) * r * (w ? w[j] : 1.f) + (b ? b[j] : 0.f));
+}
+
+// Backward, rows in registers.  A block of kTpr threads owns every gridDim.x-th
+// row and adds up its columns of dw and db in registers over its rows, so those
+// sums cost no extra pass; the blocks' partial sums [block][2][N] are added in a
+// fixed order by sum_parts_kernel.
+template <typename T, int kTpr, int kVpt>
+__global__ void __launch_bounds__(kTpr)
+    bwd_kernel(const T* __restrict__ dy, long long lddy, const T* __restrict__ x, long long ldx,
+               const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
+               T* __restrict__ dx, long long lddx, float* __restrict__ part, int M, int N) {
+    constexpr int kE = Pack<T, true>::kN;
+    __shared__ float2 sred[2][kTpr / 32];
+    const int t = threadIdx.x, nvec = N / kE;
+    float aw[kVpt][kE], ab[kVpt][kE];
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i)
+#pragma unroll
+        for (int u = 0; u < kE; ++u) aw[i][u] = ab[i][u] = 0.f;
+    Raw<T, true> rx[kVpt], rd[kVpt];
+    auto load = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            const int j = t + i * kTpr;
+            if (j < nvec) {
+                rx[i].load(x + row * ldx + (size_t)j * kE);
+                rd[i].load(dy + row * lddy + (size_t)j * kE);
+            } else {
+                rx[i].zero();
+                rd[i].zero();
+            }
+        }
+    };
+    int buf = 0;
+    for (long long row = blockIdx.x; row < M; row += gridDim.x, buf ^= 1) {
+        load(row);
+        const float mu = mean[row], r = rstd[row];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            const int j = t + i * kTpr;
+            if (j >= nvec) break;
+            float fx[kE], fd[kE];
+            rx[i].get(fx);
+            rd[i].get(fd);
+#pragma unroll
+            for (int u = 0; u < kE; u += 4) {
+                const float4 ww = w ? *reinterpret_cast<const float4*>(w + (size_t)j * kE + u) : make_float4(1, 1, 1, 1);
+                const float wv[4] = {ww.x, ww.y, ww.z, ww.w};
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float xh = (fx[u + v] - mu) * r, c = fd[u + v] * wv[v];
+                    s0 += c;
+                    s1 += c * xh;
+                    aw[i][u + v] += fd[u + v] * xh;
+                    ab[i][u + v] += fd[u + v];
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+        }
+        // two buffers: a block's next row writes the other one, and the barrier of that
+        // row comes before this buffer is written again
+        if ((t & 31) == 0) sred[buf][t >> 5] = make_float2(s0, s1);
+        __syncthreads();
+        s0 = s1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < kTpr / 32; ++k) {
+            s0 += sred[buf][k].x;
+            s1 += sred[buf][k].y;
+        }
+        s0 /= float(N);
+        s1 /= float(N);
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            const int j = t + i * kTpr;
+            if (j >= nvec) break;
+            float fx[kE], fd[kE];
+            rx[i].get(fx);
+            rd[i].get(fd);
+#pragma unroll
+            for (int u = 0; u < kE; u += 4) {
+                const float4 ww = w ? *reinterpret_cast<const float4*>(w + (size_t)j * kE + u) : make_float4(1, 1, 1, 1);
+                const float wv[4] = {ww.x, ww.y, ww.z, ww.w};
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float xh = (fx[u + v] - mu) * r;
+                    fd[u + v] = r * (fd[u + v] * wv[v] - s0 - xh * s1);
+                }
+            }
+            rd[i].set(fd);
+            rd[i].store(dx + row * lddx + (size_t)j * kE);
+        }
+    }
+    if (part) {
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            const int j = t + i * kTpr;
+            if (j >= nvec) break;
+            float* p = part + (size_t)blockIdx.x * 2 * N + (size_t)j * kE;
+#pragma unroll
+            for (int u = 0; u < kE; u += 4) {
+                *reinterpret_cast<float4*>(p + u) = make_float4(aw[i][u], aw[i][u + 1], aw[i][u + 2], aw[i][u + 3]);
+                *reinterpret_cast<float4*>(p + N + u) = make_float4(ab[i][u], ab[i][u + 1], ab[i][u + 2], ab[i][u + 3]);
+            }
+        }
+    }
+}
+
+// Any width and alignment: dx row by row, then the column sums in a second walk.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    bwd_any_kernel(const T* __restrict__ dy, long long lddy, const T* __restrict__ x, long long ldx,
+                   const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
+                   T* __restrict__ dx, long long lddx, int N) {
+    __shared__ float sred[2][8];
+    const long long row = blockIdx.x;
+    const T *xr = x + row * ldx, *dr = dy + row * lddy;
+    const float mu = mean[row], r = rstd[row];
+    float s0 = 0.f, s1 = 0.f;
+    for (int j = threadIdx.x; j < N; j += 256) {
+        const float c = __fmul_rn(to_f32<T>(dr[j]), w ? w[j] : 1.f);  // rounded as below: c - mean(c) is exactly 0 at N = 1
+        s0 += c;
+        s1 += c * (to_f32<T>(xr[j]) - mu) * r;
+    }
+    s0 = row_sum<256>(s0, sred[0]) / float(N);
+    s1 = row_sum<256>(s1, sred[1]) / float(N);
+    T* dxr = dx + row * lddx;
+    for (int j = threadIdx.x; j < N; j += 256) {
+        const float xh = (to_f32<T>(xr[j]) - mu) * r;
+        dxr[j] = from_f32<T>(r * (__fmul_rn(to_f32<T>(dr[j]), w ? w[j] : 1.f) - s0 - xh * s1));
+    }
+}
+// Thread = one column, block row = a run of rows: partial sums [gridDim.y][2][N].
+template <typename T>
+__global__ void __launch_bounds__(128)
+    bwd_any_cols_kernel(const T* __restrict__ dy, long long lddy, const T* __restrict__ x, long long ldx,
+                        const float* __restrict__ mean, const float* __restrict__ rstd, float* __restrict__ part, int M,
+                        int N) {
+    const int j = blockIdx.x * 128 + threadIdx.x;
+    if (j >= N) return;
+    float aw = 0.f, ab = 0.f;
+#pragma unroll 4
+    for (long long row = blockIdx.y; row < M; row += gridDim.y) {
+        const float d = to_f32<T>(dy[row * lddy + j]);
+        aw += d * (to_f32<T>(x[row * ldx + j]) - mean[row]) * rstd[row];
+        ab += d;
+    }
+    part[(size_t)blockIdx.y * 2 * N + j] = aw;
+    part[(size_t)blockIdx.y * 2 * N + N + j] = ab;
+}
+
+// Threads and vectors per thread that hold a row of nvec vectors.
+struct Shape {
+    int tpr, vpt;  // vpt 0: no fit
+};
+static Shape bwd_shape(int nvec) {
+    if (nvec <= 64) return {32, nvec <= 32 ? 1 : 2};
+    if (nvec <= 256) return {128, nvec <= 128 ? 1 : 2};
+    if (nvec <= 512) return {256, 2};
+    if (nvec <= 2048) return {512, nvec <= 1024 ? 2 : 4};
+    return {0, 0};
+}
+
+static bool vec_ok(int N, int es, const void* const* ptrs, const long long* lds, int n) {
+    if ((N * es) % 16) return false;
+    for (int i = 0; i < n; ++i)
+        if (!al16(ptrs[i]) || (lds[i] * es) % 16) return false;
+    return true;
+}
+
+// Blocks of the backward pass: enough to fill the SMs at the register use of the
+// shape, and no more than there are rows (each block writes 2 N partial sums).
+static int bwd_blocks(int M, int tpr) {
+    const long long want = (long long)device_sm_count() * (tpr >= 512 ? 1 : (tpr == 256 ? 2 : (tpr == 128 ? 4 : 12)));
+    return int(M < want ? M : want);
+}
+static int any_blocks(int M) { return M < 256 ? M : 256; }
+
+template <typename T>
+int fwd(const T* x, long long ldx, const float* w, const float* b, T* y, long long ldy, float* mean, float* rstd, int M,
+        int N, float eps, cudaStream_t st) {
+    constexpr int es = sizeof(T), kE = 16 / es;
+    const void* ptrs[] = {x, y, w, b};
+    const long long lds[] = {ldx, ldy, 0, 0};
+    const int nvec = N / kE;
+    if (vec_ok(N, es, ptrs, lds, 4) && nvec <= 2048) {
+#define KDA_LN_FWD(TPR, VPT)                                                                                       \
+    fwd_kernel<T, TPR, VPT><<<unsigned(TPR >= 128 ? M : cdiv(M, 128 / TPR)), TPR > 128 ? TPR : 128, 0, st>>>(      \
+        x, ldx, w, b, y, ldy, mean, rstd, M, N, eps)
+        if (nvec <= 32) KDA_LN_FWD(32, 1);
+        else if (nvec <= 64) KDA_LN_FWD(32, 2);
+        else if (nvec <= 128) KDA_LN_FWD(32, 4);
+        else if (nvec <= 256) KDA_LN_FWD(128, 2);
+        else if (nvec <= 512) KDA_LN_FWD(256, 2);
+        else if (nvec <= 1024) KDA_LN_FWD(256, 4);
+        else KDA_LN_FWD(512, 4);
+#undef KDA_LN_FWD
+    } else {
+        fwd_any_kernel<T><<<unsigned(M), 256, 0, st>>>(x, ldx, w, b, y, ldy, mean, rstd, N, eps);
+    }
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+template <typename T>
+int bwd(const T* dy, long long lddy, const T* x, long long ldx, const float* w, const float* mean, const float* rstd,
+        T* dx, long long lddx, float* dw, float* db, int M, int N, float* part, cudaStream_t st) {
+    constexpr int es = sizeof(T), kE = 16 / es;
+    const void* ptrs[] = {dy, x, dx, w};
+    const long long lds[] = {lddy, ldx, lddx, 0};
+    const Shape sh = bwd_shape(N / kE);
+    int parts;
+    if (vec_ok(N, es, ptrs, lds, 4) && sh.vpt) {
+        parts = bwd_blocks(M, sh.tpr);
+        float* p = (dw || db) ? part : nullptr;
+#define KDA_LN_BWD(TPR, VPT) \
+    if (sh.tpr == TPR && sh.vpt == VPT) \
+    bwd_kernel<T, TPR, VPT><<<parts, TPR, 0, st>>>(dy, lddy, x, ldx, w, mean, rstd, dx, lddx, p, M, N)
+        KDA_LN_BWD(32, 1);
+        KDA_LN_BWD(32, 2);
+        KDA_LN_BWD(128, 1);
+        KDA_LN_BWD(128, 2);
+        KDA_LN_BWD(256, 2);
+        KDA_LN_BWD(512, 2);
+        KDA_LN_BWD(512, 4);
+#undef KDA_LN_BWD
+    } else {
+        bwd_any_kernel<T><<<unsigned(M), 256, 0, st>>>(dy, lddy, x, ldx, w, mean, rstd, dx, lddx, N);
+        parts = any_blocks(M);
+        if (dw || db)
+            bwd_any_cols_kernel<T><<<dim3(unsigned(cdiv(N, 128)), parts), 128, 0, st>>>(dy, lddy, x, ldx, mean, rstd,
+                                                                                        part, M, N);
+    }
+    if (dw) sum_parts_kernel<float><<<unsigned(cdiv(N, 32)), 256, 0, st>>>(part, parts, 2ll * N, dw, N);
+    if (db) sum_parts_kernel<float><<<unsigned(cdiv(N, 32)), 256, 0, st>>>(part + N, parts, 2ll * N, db, N);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace norm
+
+size_t layer_norm_bwd_workspace_bytes(int M, int N) {
+    // whichever path the call takes (its type and alignment decide): the most blocks of any
+    int parts = norm::any_blocks(M);
+    for (int e = 4; e <= 8; e += 4) {
+        const norm::Shape sh = norm::bwd_shape(N / e);
+        if (sh.vpt && norm::bwd_blocks(M, sh.tpr) > parts) parts = norm::bwd_blocks(M, sh.tpr);
+    }
+    return mix::up256(size_t(parts) * 2 * N * sizeof(float));
+}
+
+int launch_layer_norm_fwd(const void* x, long long ldx, const float* w, const float* b, void* y, long long ldy,
+                          float* mean, float* rstd, int M, int N, int dtype, float eps, cudaStream_t st) {
+    if (dtype == KDA_BF16)
+        return norm::fwd(static_cast<const __nv_bfloat16*>(x), ldx, w, b, static_cast<__nv_bfloat16*>(y), ldy, mean,
+                         rstd, M, N, eps, st);
+    return norm::fwd(static_cast<const float*>(x), ldx, w, b, static_cast<float*>(y), ldy, mean, rstd, M, N, eps, st);
+}
+
+int launch_layer_norm_bwd(const void* dy, long long lddy, const void* x, long long ldx, const float* w,
+                          const float* mean, const float* rstd, void* dx, long long lddx, float* dw, float* db, int M,
+                          int N, int dtype, void* ws, cudaStream_t st) {
+    float* part = static_cast<float*>(ws);
+    if (dtype == KDA_BF16)
+        return norm::bwd(static_cast<const __nv_bfloat16*>(dy), lddy, static_cast<const __nv_bfloat16*>(x), ldx, w,
+                         mean, rstd, static_cast<__nv_bfloat16*>(dx), lddx, dw, db, M, N, part, st);
+    return norm::bwd(static_cast<const float*>(dy), lddy, static_cast<const float*>(x), ldx, w, mean, rstd,
+                     static_cast<float*>(dx), lddx, dw, db, M, N, part, st);
+}
+
+}  // namespace kda

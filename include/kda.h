@@ -451,6 +451,183 @@ size_t kda_layer_decode_workspace(int B, int T, int d_model, int H, int rank);
 int kda_layer_decode(const void *x, const kda_layer_weights *w, void *conv_state, float *state, void *y,
                      int B, int T, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ========================================================================
+ * The parts of a selective state-space mixer: layer norm, a projection with a
+ * bias, an activation and a residual, the short causal convolution and the
+ * selective scan, each with its gradients and its form for single tokens.
+ * No counterpart on the pages beyond the ShortConv and the projections of
+ * "Neural Parameterization"; they stand next to the KDA layer's own steps.
+ *
+ * Conventions on top of those above: token tensors here have a row stride
+ * ("ld...", in elements, at least the row), so that a slice of a wider
+ * projection can be passed; token t of batch row b is row b*T + t of a
+ * dense tensor.  Rows that start on 16-byte boundaries
+ * and divide into 16-byte vectors are the fast path; any other alignment of
+ * the element type, stride or width is accepted unless stated.  Outputs must
+ * not overlap inputs except where stated.
+ * ======================================================================== */
+
+/* ------------------------------------------------------------------------
+ * kda_layer_norm_fwd / kda_layer_norm_bwd -- layer norm over the last axis.
+ *
+ *     y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps)
+ *     dx = rstd * (c - mean(c) - xh * mean(c * xh)), c = weight * dy, xh = (x - mean) * rstd
+ *     dweight = sum over rows of dy * xh,  dbias = sum over rows of dy
+ *
+ *   x, y, dy, dx   [M, N], dtype bf16 or fp32 (one type for all).  N >= 1.
+ *   weight, bias   fp32 [N] or NULL (1 and 0).
+ *   mean, rstd     fp32 [M]: written by the forward pass when not NULL, read
+ *                  (required) by the backward pass.
+ *   dweight, dbias fp32 [N] or NULL (not computed).
+ *   workspace      kda_layer_norm_bwd_workspace(M, N) bytes, 256-byte aligned;
+ *                  may be NULL when dweight and dbias both are.
+ * Statistics and sums are fp32, in a fixed order.  M = 0 zeroes dweight, dbias.
+ */
+int kda_layer_norm_fwd(const void *x, long long ldx, const float *weight, const float *bias, void *y, long long ldy,
+                       float *mean, float *rstd, int M, int N, int dtype, float eps, void *stream);
+
+size_t kda_layer_norm_bwd_workspace(int M, int N);
+
+int kda_layer_norm_bwd(const void *dy, long long lddy, const void *x, long long ldx, const float *weight,
+                       const float *mean, const float *rstd, void *dx, long long lddx, float *dweight, float *dbias,
+                       int M, int N, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * kda_linear_act_bf16 / kda_linear_act_bwd_bf16 -- a projection with its
+ * epilogue, and its gradients.
+ *
+ *     s = x W^T + bias,  y = act(s) + residual
+ *     ds = dy * act'(s),  dx = ds W,  dW = ds^T x,  dbias = sum over rows of ds
+ * (the residual's gradient is dy).
+ *
+ *   x   bf16 [M, K];  W  bf16 [N, K];  y, residual, pre, dy  bf16 [M, N];
+ *   bias, dbias  fp32 [N] or NULL;  dx  bf16 [M, K], dW  bf16 [N, K] or NULL.
+ *   act   a kda_activation; GELU is x * Phi(x), with the error function.
+ *   pre   NULL, or the output that keeps s for the backward pass (forward);
+ *         the kept s, required unless act is KDA_ACT_NONE (backward).
+ * x, W, y, pre (forward), dx and dW: 16-byte aligned, row strides multiples of
+ * 8 elements.  residual, and dy and pre of the backward pass: any alignment
+ * and stride.  fp32 accumulation; bias, activation and residual are applied to
+ * the fp32 sum and y is rounded once.  The backward pass rounds ds to bf16 (the
+ * operand of its two products); dbias sums the unrounded ds.
+ *   workspace  kda_linear_act_bwd_workspace(M, N) bytes, 256-byte aligned.
+ */
+typedef enum {
+    KDA_ACT_NONE = 0,
+    KDA_ACT_RELU = 1,
+    KDA_ACT_GELU = 2,
+    KDA_ACT_SILU = 3,
+    KDA_ACT_SOFTPLUS = 4
+} kda_activation;
+
+int kda_linear_act_bf16(const void *x, int ldx, const void *W, int ldw, const float *bias, const void *residual,
+                        int ldr, void *y, int ldy, void *pre, int ldp, int M, int N, int K, int act, void *stream);
+
+size_t kda_linear_act_bwd_workspace(int M, int N);
+
+int kda_linear_act_bwd_bf16(const void *dy, int lddy, const void *x, int ldx, const void *W, int ldw, const void *pre,
+                            int ldp, void *dx, int lddx, void *dW, int lddw, float *dbias, int M, int N, int K, int act,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * kda_short_conv_* -- short causal depthwise convolution with an optional SiLU.
+ *
+ *     s_t = bias + sum_j w[c][j] x_{t-(width-1)+j},  y_t = SiLU(s_t) if silu else s_t
+ * "Kimi Linear: An Expressive, Efficient Attention Architecture", section "Neural
+ * Parameterization" (depthwise ShortConv, kernel 4, then SiLU), on its own, for
+ * widths 2, 3 and 4, with a bias and gradients.
+ *
+ *   x, y, dy, dx   [B, T, C] or packed [1, Ttot, C] with cu_seqlens (as in
+ *                  kda_chunk_fwd; num_seqs = 0 for dense), dtype bf16 or fp32.
+ *   w, dw          [C, width], same dtype;  bias, dbias fp32 [C] or NULL.
+ *   conv_state_in / conv_state_out  [N, width-1, C], same dtype, or NULL: the last
+ *                  width-1 inputs before / at the end of each sequence, oldest
+ *                  first (NULL in = zeros).  A sequence shorter than that keeps the
+ *                  tail of its incoming state.  The two may be the same buffer.
+ *   backward:      d_conv_state_out, d_conv_state_in likewise, or NULL; workspace of
+ *                  kda_short_conv_bwd_workspace(B*T, C, width) bytes, 256-byte
+ *                  aligned.  dw and dbias are summed in a fixed order in fp32.
+ *   step:          one token for each of B sequences: x, y [B, C]; conv_state
+ *                  [B, width-1, C] is moved up one row in place.
+ */
+int kda_short_conv_fwd(const void *x, long long ldx, const void *w, const float *bias, void *y, long long ldy,
+                       const void *conv_state_in, void *conv_state_out, const int32_t *cu_seqlens, int num_seqs, int B,
+                       int T, int C, int width, int dtype, int silu, void *stream);
+
+size_t kda_short_conv_bwd_workspace(int tokens, int C, int width);
+
+int kda_short_conv_bwd(const void *dy, long long lddy, const void *x, long long ldx, const void *w, const float *bias,
+                       const void *conv_state_in, const void *d_conv_state_out, void *dx, long long lddx, void *dw,
+                       float *dbias, void *d_conv_state_in, const int32_t *cu_seqlens, int num_seqs, int B, int T,
+                       int C, int width, int dtype, int silu, void *workspace, size_t workspace_bytes, void *stream);
+
+int kda_short_conv_step(const void *x, long long ldx, const void *w, const float *bias, void *conv_state, void *y,
+                        long long ldy, int B, int C, int width, int dtype, int silu, void *stream);
+
+/* ------------------------------------------------------------------------
+ * kda_selective_scan_* -- the selective state-space recurrence.
+ *
+ *     D_t = softplus(dt_t + dt_bias)            (dt_t + dt_bias without dt_softplus)
+ *     h_t[d][n] = exp(D_t[d] A[d][n]) h_{t-1}[d][n] + D_t[d] u_t[d] B_t[g][n]
+ *     y_t[d] = (sum_n C_t[g][n] h_t[d][n] + D[d] u_t[d]) * SiLU(z_t[d])
+ * with channel d in group g = d / (channels / groups).
+ *
+ *   u, dt, z, y    [B, T, channels] or packed [1, Ttot, channels] with cu_seqlens,
+ *                  dtype bf16 or fp32; z NULL: no gate.
+ *   B, C           [B, T, groups, state] of the same dtype; the row stride is that
+ *                  from token to token, groups and states are contiguous.
+ *   A              fp32 [channels, state];  D, dt_bias fp32 [channels] or NULL.
+ *   initial_state / final_state  fp32 [N, channels, state] or NULL (zero / not
+ *                  written); they may be the same buffer.
+ *   1 <= state <= 32; channels is a multiple of groups.
+ *   workspace      kda_selective_scan_fwd_workspace(...) bytes (0: may be NULL),
+ *                  256-byte aligned.
+ * States and sums are fp32.  Sequences that are too few for the SMs are cut into
+ * segments whose maps are composed; the result is the recurrence's up to rounding,
+ * and the same on every run.
+ *
+ * kda_selective_scan_bwd: given dy and d_final_state (or NULL), writes du, ddt, dz
+ * [B, T, channels] (dz when z is given), dB, dC [B, T, groups, state], all of the
+ * dtype; dA fp32 [channels, state], dD and ddt_bias fp32 [channels] or NULL,
+ * d_initial_state fp32 or NULL.  Workspace: per token, channels x state / 2 bytes
+ * of states (state 16) and groups x state x channels / (4 x groups) bytes of partial
+ * sums; see kda_selective_scan_bwd_workspace().
+ *
+ * kda_selective_scan_step: one token for each of B sequences, state [B, channels,
+ * state] updated in place; u, dt, z, y [B, channels], B, C [B, groups, state].
+ */
+typedef struct {
+    const float *A;
+    const float *D;
+    const float *dt_bias;
+    int channels;
+    int groups;
+    int state;
+    int dt_softplus;
+} kda_scan_params;
+
+size_t kda_selective_scan_fwd_workspace(int B, int T, int channels, int groups, int state, int num_seqs);
+
+int kda_selective_scan_fwd(const void *u, long long ldu, const void *dt, long long lddt, const void *B, long long ldb,
+                           const void *C, long long ldc, const void *z, long long ldz, const kda_scan_params *params,
+                           const float *initial_state, float *final_state, void *y, long long ldy,
+                           const int32_t *cu_seqlens, int num_seqs, int batch, int T, int dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+size_t kda_selective_scan_bwd_workspace(int B, int T, int channels, int groups, int state, int num_seqs);
+
+int kda_selective_scan_bwd(const void *dy, long long lddy, const void *u, long long ldu, const void *dt, long long lddt,
+                           const void *B, long long ldb, const void *C, long long ldc, const void *z, long long ldz,
+                           const kda_scan_params *params, const float *initial_state, const float *d_final_state,
+                           void *du, long long lddu, void *ddt, long long ldddt, void *dB, long long lddb, void *dC,
+                           long long lddc, void *dz, long long lddz, float *dA, float *dD, float *ddt_bias,
+                           float *d_initial_state, const int32_t *cu_seqlens, int num_seqs, int batch, int T, int dtype,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+int kda_selective_scan_step(const void *u, long long ldu, const void *dt, long long lddt, const void *B, long long ldb,
+                            const void *C, long long ldc, const void *z, long long ldz, const kda_scan_params *params,
+                            float *state, void *y, long long ldy, int batch, int dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
