@@ -81,28 +81,43 @@ __device__ __forceinline__ void load_taps(const T* w, int c0, float (&f)[kE][W])
     }
 }
 
-// A block: 128 vectors of channels (blockIdx.y) by kTok tokens (blockIdx.x).  All
-// rows of the run are requested before the first is used.
-template <typename T, int W, bool kVec, int kTok>
-__global__ void __launch_bounds__(128) fwd_kernel(const Args a) {
-    constexpr int kE = Pack<T, kVec>::kN;
+// A block: 128 vectors of channels (blockIdx.y) by a run of tokens (blockIdx.x).  A
+// thread keeps kRing rows in flight: each row's register is requested again, kRing
+// tokens ahead, as soon as its value has been used.
+template <typename T, int W, bool kVec, int kRing>
+__global__ void __launch_bounds__(128) fwd_kernel(const Args a, int run) {
+    constexpr int kE = Pack<T, kVec>::kN, kP = kE > 1 ? kE / 2 : 1;
     const int c0 = (blockIdx.y * 128 + threadIdx.x) * kE;
     if (c0 >= a.C) return;
     const T* x = static_cast<const T*>(a.x) + c0;
     T* y = static_cast<T*>(a.y) + c0;
     const T* in = static_cast<const T*>(a.cache_in);
-    const int t0 = blockIdx.x * kTok, t1 = min(a.ntok, t0 + kTok);
-    Raw<T, kVec> rows[kTok];
+    const int t0 = blockIdx.x * run, t1 = min(a.ntok, t0 + run);
+    Raw<T, kVec> ring[kRing];
 #pragma unroll
-    for (int j = 0; j < kTok; ++j)
-        if (t0 + j < t1) rows[j].load(x + (long long)(t0 + j) * a.ldx);
-    float w[kE][W], b[kE];
-    load_taps<T, W, kE>(static_cast<const T*>(a.w), c0, w);
+    for (int j = 0; j < kRing; ++j)
+        if (t0 + j < t1) ring[j].load_stream(x + (long long)(t0 + j) * a.ldx);
+    // channels in pairs (one channel on its own in the scalar form)
+    f2 w[W][kP], b[kP], h[W - 1][kP];  // h: inputs at t-(W-1) .. t-1
+    {
+        float wf[kE][W];
+        load_taps<T, W, kE>(static_cast<const T*>(a.w), c0, wf);
 #pragma unroll
-    for (int u = 0; u < kE; ++u) b[u] = a.bias ? a.bias[c0 + u] : 0.f;
+        for (int u = 0; u < kP; ++u) {
+            constexpr int o = kE > 1 ? 1 : 0;
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][u] = pk(wf[2 * u * o][j], wf[2 * u * o + o][j]);
+            b[u] = a.bias ? pk(a.bias[c0 + 2 * u * o], a.bias[c0 + 2 * u * o + o]) : 0ull;
+        }
+    }
+    auto get2 = [](const Raw<T, kVec>& r, f2 (&v)[kP]) {
+        float f[kE];
+        r.get(f);
+#pragma unroll
+        for (int u = 0; u < kP; ++u) v[u] = kE > 1 ? pk(f[2 * u], f[kE > 1 ? 2 * u + 1 : 0]) : pk(f[0], 0.f);
+    };
     int n = seq_of(a.cu, a.nseq, a.seq_len, t0);
     int s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
-    float h[W - 1][kE];  // inputs at t-(W-1) .. t-1
     auto history = [&](int t) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
@@ -111,37 +126,49 @@ __global__ void __launch_bounds__(128) fwd_kernel(const Args a) {
             if (p >= s_beg) r.load(x + (long long)p * a.ldx);
             else if (in) r.load(in + ((size_t)n * (W - 1) + (W - 1 + p - s_beg)) * a.C + c0);
             else r.zero();
-            r.get(h[j]);
+            get2(r, h[j]);
         }
     };
     history(t0);
+    for (int tb = t0; tb < t1; tb += kRing) {
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-        const int t = t0 + i;
-        if (t >= t1) break;
-        if (t >= s_end) {  // a new sequence starts at t (empty ones are skipped)
-            while (t >= s_end && n + 1 < a.nseq) {
-                ++n;
-                s_beg = s_end;
-                s_end = seq_begin(a.cu, a.seq_len, n + 1);
+        for (int i = 0; i < kRing; ++i) {
+            const int t = tb + i;
+            if (t >= t1) break;
+            if (t >= s_end) {  // a new sequence starts at t (empty ones are skipped)
+                while (t >= s_end && n + 1 < a.nseq) {
+                    ++n;
+                    s_beg = s_end;
+                    s_end = seq_begin(a.cu, a.seq_len, n + 1);
+                }
+                history(t);
             }
-            history(t);
+            f2 v[kP];
+            get2(ring[i], v);
+            if (t + kRing < t1) ring[i].load_stream(x + (long long)(t + kRing) * a.ldx);
+            float o[kE];
+#pragma unroll
+            for (int u = 0; u < kP; ++u) {
+                f2 s = b[u];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) s = fma2(w[j][u], h[j][u], s);
+                s = fma2(w[W - 1][u], v[u], s);
+                float s0, s1;
+                upk(s, s0, s1);
+                if (a.silu) {
+                    s0 = __fdividef(s0, 1.f + __expf(-s0));
+                    if (kE > 1) s1 = __fdividef(s1, 1.f + __expf(-s1));
+                }
+                o[kE > 1 ? 2 * u : 0] = s0;
+                if constexpr (kE > 1) o[2 * u + 1] = s1;
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) h[j][u] = h[j + 1][u];
+                h[W - 2][u] = v[u];
+            }
+            Raw<T, kVec> r;
+            r.set(o);
+            r.store(y + (long long)t * a.ldy);
         }
-        float v[kE], o[kE];
-        rows[i].get(v);
-#pragma unroll
-        for (int u = 0; u < kE; ++u) {
-            float s = b[u];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) s += w[u][j] * h[j][u];
-            s += w[u][W - 1] * v[u];
-            o[u] = a.silu ? __fdividef(s, 1.f + __expf(-s)) : s;
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) h[j][u] = h[j + 1][u];
-            h[W - 2][u] = v[u];
-        }
-        rows[i].set(o);
-        rows[i].store(y + (long long)t * a.ldy);
     }
 }
 
@@ -404,7 +431,15 @@ __global__ void __launch_bounds__(128) step_kernel(const Args a, T* __restrict__
     h[0].store(static_cast<T*>(a.y) + n * a.ldy + c0);
 }
 
-constexpr int kFwdTok = 12;
+constexpr int kFwdRing = 8;
+
+// Tokens of one thread in the forward pass: long runs re-read few rows (W - 1 per run),
+// short ones fill the SMs.
+static int fwd_run(int ntok, int C, int kE) {
+    const long long lanes = cdiv(cdiv(C, kE), 128);
+    const long long want = cdiv((long long)ntok * lanes, (long long)device_sm_count() * 16);
+    return int(want < 8 ? 8 : (want > 64 ? 64 : want));
+}
 
 // Tokens of one thread in the backward pass: long runs write few partial sums
 // ((W + 1) x 4 bytes per channel and run), short ones fill the SMs.
@@ -418,9 +453,10 @@ template <typename T, int W>
 int fwd(const Args& a, bool vec, cudaStream_t st) {
     if (a.ntok > 0) {
         const int kE = vec ? int(16 / sizeof(T)) : 1;
-        const dim3 grid(unsigned(cdiv(a.ntok, kFwdTok)), unsigned(cdiv(cdiv(a.C, kE), 128)));
-        if (vec) fwd_kernel<T, W, true, kFwdTok><<<grid, 128, 0, st>>>(a);
-        else fwd_kernel<T, W, false, kFwdTok><<<grid, 128, 0, st>>>(a);
+        const int run = fwd_run(a.ntok, a.C, kE);
+        const dim3 grid(unsigned(cdiv(a.ntok, run)), unsigned(cdiv(cdiv(a.C, kE), 128)));
+        if (vec) fwd_kernel<T, W, true, kFwdRing><<<grid, 128, 0, st>>>(a, run);
+        else fwd_kernel<T, W, false, kFwdRing><<<grid, 128, 0, st>>>(a, run);
     }
     if (a.cache_out) {  // after the main kernel on the stream, so cache_out may be cache_in
         const long long n = cdiv((long long)a.nseq * a.C, 256);

@@ -518,7 +518,7 @@ int launch_linear_act_bwd(const void* dy, int lddy, const void* x, int ldx, cons
         if (vec) lin::act_grad_kernel<true><<<grid, 256, 0, st>>>(d, lddy, s, ldp, ds, pl.ldds, part, M, N, rows, act);
         else lin::act_grad_kernel<false><<<grid, 256, 0, st>>>(d, lddy, s, ldp, ds, pl.ldds, part, M, N, rows, act);
         if (part)
-            mix::sum_parts_kernel<float><<<unsigned(mix::cdiv(N, 32)), 256, 0, st>>>(part, parts, N, dbias, N);
+            mix::sum_parts<float>(part, parts, N, dbias, nullptr, N, st);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) {
             *why = cudaGetErrorString(e);

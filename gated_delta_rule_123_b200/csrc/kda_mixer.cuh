@@ -64,6 +64,88 @@ struct Raw {
     __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<type*>(p) = v; }
 };
 
+// Two fp32 values in one 64-bit register pair: Blackwell's packed instructions do both
+// in one issue slot (the kernels here are bound by issue and by the special-function
+// unit where they are not bound by HBM).
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pk(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void upk(f2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ float lo2(f2 v) {
+    float a, b;
+    upk(v, a, b);
+    return a;
+}
+__device__ __forceinline__ float hi2(f2 v) {
+    float a, b;
+    upk(v, a, b);
+    return b;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 dup2(float v) { return pk(v, v); }
+
+// 2^x on the special-function unit (relative error about 2^-22; below 2^-126 it gives 0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kL2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// log(1 + e^x) = max(x, 0) + log1p(e^-|x|).  log1p(e) / e on [0, 1] is its Chebyshev
+// interpolant of degree 9 (relative error 1.2e-7 with fp32 coefficients and steps, also
+// where e is tiny): no second special function, and no branch.
+__device__ __forceinline__ float softplus_poly(float x) {
+    const float e = ex2(-fabsf(x) * kL2e);
+    float r = fmaf(-0.0031760570127516985f, e, 0.019542526453733444f);
+    r = fmaf(r, e, -0.056373611092567444f);
+    r = fmaf(r, e, 0.10543623566627502f);
+    r = fmaf(r, e, -0.1526966691017151f);
+    r = fmaf(r, e, 0.1966327428817749f);
+    r = fmaf(r, e, -0.24951615929603577f);
+    r = fmaf(r, e, 0.33329710364341736f);
+    r = fmaf(r, e, -0.49999892711639404f);
+    r = fmaf(r, e, 1.f);
+    return fmaf(r, e, fmaxf(x, 0.f));
+}
+// x / (1 + e^-x); -0 where e^-x overflows.
+__device__ __forceinline__ float siluf(float x) { return x * rcp(1.f + ex2(-x * kL2e)); }
+
+// 16, 8 or 4 bytes of global memory into shared memory, asynchronously.
+template <int kBytes>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+    static_assert(kBytes == 4 || kBytes == 8 || kBytes == 16, "cp.async size");
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
 __device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 // log(1 + e^x) without overflow, and with e^x's relative accuracy for very negative x.
 __device__ __forceinline__ float softplusf(float x) { return fmaxf(x, 0.f) + log1pf(__expf(-fabsf(x))); }
@@ -72,32 +154,40 @@ inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) 
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
-// out[i] = sum over p of part[p * stride + i], i < n, in a fixed order: 8 threads
-// walk every 8th part each, then their sums are added.  Bound by reading the
-// partial sums once.
+// out[i] = sum over p of part[p * stride + i], i < n, in a fixed order: 32 threads
+// add every 32nd part each, then their sums are added.  Two outputs of n columns side
+// by side in the parts (n each, the second may be NULL) go in one launch.  Bound by
+// the latency of a thread's chain of loads, so the chain is short and unrolled:
+// 592 parts of 4096 columns take 4 us (with 8 threads a column, 20 us).
 template <typename Out>
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, int parts, long long stride,
-                                                        Out* __restrict__ out, long long n) {
-    __shared__ float s[8][33];
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, int parts, long long stride,
+                                                         Out* __restrict__ out, Out* __restrict__ out2, long long n) {
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const long long i = (long long)blockIdx.x * 32 + lane;
-    float a = 0.f, b = 0.f;
+    const long long blocks1 = (n + 31) / 32;
+    const bool second = blockIdx.x >= blocks1;
+    const long long i = (blockIdx.x - (second ? blocks1 : 0)) * 32 + lane;
+    Out* o = second ? out2 : out;
+    if (!o) return;
+    float a = 0.f;
     if (i < n) {
-        int p = row;
-        for (; p + 8 < parts; p += 16) {
-            a += part[p * stride + i];
-            b += part[(p + 8) * stride + i];
-        }
-        if (p < parts) a += part[p * stride + i];
+        const float* q = part + (second ? n : 0) + i;
+#pragma unroll 8
+        for (int p = row; p < parts; p += 32) a += q[p * stride];
     }
-    s[row][lane] = a + b;
+    s[row][lane] = a;
     __syncthreads();
     if (row == 0 && i < n) {
         float t = 0.f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) t += s[r][lane];
-        out[i] = from_f32<Out>(t);
+        for (int r = 0; r < 32; ++r) t += s[r][lane];
+        o[i] = from_f32<Out>(t);
     }
+}
+template <typename Out>
+inline void sum_parts(const float* part, int parts, long long stride, Out* out, Out* out2, long long n, cudaStream_t st) {
+    if (!out && !out2) return;
+    sum_parts_kernel<Out><<<unsigned(cdiv(n, 32) * (out2 ? 2 : 1)), 1024, 0, st>>>(part, parts, stride, out, out2, n);
 }
 
 }  // namespace mix

@@ -252,7 +252,7 @@ int kda_short_conv_step(const void* x, long long ldx, const void* w, const float
 size_t kda_selective_scan_fwd_workspace(int B, int T, int channels, int groups, int state, int num_seqs) {
     if (B <= 0 || T <= 0 || channels <= 0 || groups <= 0 || state <= 0 || state > 32 || channels % groups || num_seqs < 0)
         return 0;
-    return selective_scan_fwd_workspace_bytes(B, T, channels, groups, state, num_seqs > 0);
+    return selective_scan_fwd_workspace_bytes(B, T, channels, groups, state, num_seqs);
 }
 
 int kda_selective_scan_fwd(const void* u, long long ldu, const void* dt, long long lddt, const void* B, long long ldb,
@@ -281,7 +281,7 @@ int kda_selective_scan_fwd(const void* u, long long ldu, const void* dt, long lo
         if (!aligned_es(q, dtype)) return fail(KDA_ERR_INVALID_ARG, "pointers must be aligned to their element type");
     if (y == u || y == dt || y == B || y == C || y == z) return fail(KDA_ERR_INVALID_ARG, "y must not alias an input");
     if (!cu_seqlens && batch > 65535) return fail(KDA_ERR_UNSUPPORTED, "more than 65535 rows: pack them (cu_seqlens)");
-    rc = check_workspace(workspace, workspace_bytes, selective_scan_fwd_workspace_bytes(batch, T, D, G, N, cu_seqlens != nullptr));
+    rc = check_workspace(workspace, workspace_bytes, selective_scan_fwd_workspace_bytes(batch, T, D, G, N, num_seqs));
     if (rc != KDA_OK) return rc;
     scan::SArgs a{};
     a.u = u; a.ldu = ldu; a.dt = dt; a.lddt = lddt; a.Bm = B; a.ldb = ldb; a.Cm = C; a.ldc = ldc; a.z = z; a.ldz = ldz;

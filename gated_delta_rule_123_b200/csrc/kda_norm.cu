@@ -141,24 +141,38 @@ __global__ void __launch_bounds__(kTpr)
     for (int i = 0; i < kVpt; ++i)
 #pragma unroll
         for (int u = 0; u < kE; ++u) aw[i][u] = ab[i][u] = 0.f;
-    Raw<T, true> rx[kVpt], rd[kVpt];
-    auto load = [&](long long row) {
+    // the block's next row, requested one row ahead where the registers allow it (32
+    // values a thread would spill)
+    constexpr bool kAhead = kVpt * kE <= 16;
+    Raw<T, true> nx[kVpt], nd[kVpt];
+    float nmu = 0.f, nr = 0.f;
+    auto request = [&](long long row) {
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
             const int j = t + i * kTpr;
             if (j < nvec) {
-                rx[i].load(x + row * ldx + (size_t)j * kE);
-                rd[i].load(dy + row * lddy + (size_t)j * kE);
+                nx[i].load(x + row * ldx + (size_t)j * kE);
+                nd[i].load(dy + row * lddy + (size_t)j * kE);
             } else {
-                rx[i].zero();
-                rd[i].zero();
+                nx[i].zero();
+                nd[i].zero();
             }
         }
+        nmu = mean[row];
+        nr = rstd[row];
     };
     int buf = 0;
+    if (kAhead && blockIdx.x < M) request(blockIdx.x);
     for (long long row = blockIdx.x; row < M; row += gridDim.x, buf ^= 1) {
-        load(row);
-        const float mu = mean[row], r = rstd[row];
+        if (!kAhead) request(row);
+        Raw<T, true> rx[kVpt], rd[kVpt];
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            rx[i] = nx[i];
+            rd[i] = nd[i];
+        }
+        const float mu = nmu, r = nr;
+        if (kAhead && row + gridDim.x < M) request(row + gridDim.x);
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
@@ -318,6 +332,7 @@ int fwd(const T* x, long long ldx, const float* w, const float* b, T* y, long lo
         if (nvec <= 32) KDA_LN_FWD(32, 1);
         else if (nvec <= 64) KDA_LN_FWD(32, 2);
         else if (nvec <= 128) KDA_LN_FWD(32, 4);
+        else if (nvec <= 256 && M > 4 * device_sm_count()) KDA_LN_FWD(32, 8);
         else if (nvec <= 256) KDA_LN_FWD(128, 2);
         else if (nvec <= 512) KDA_LN_FWD(256, 2);
         else if (nvec <= 1024) KDA_LN_FWD(256, 4);
@@ -358,8 +373,7 @@ int bwd(const T* dy, long long lddy, const T* x, long long ldx, const float* w, 
             bwd_any_cols_kernel<T><<<dim3(unsigned(cdiv(N, 128)), parts), 128, 0, st>>>(dy, lddy, x, ldx, mean, rstd,
                                                                                         part, M, N);
     }
-    if (dw) sum_parts_kernel<float><<<unsigned(cdiv(N, 32)), 256, 0, st>>>(part, parts, 2ll * N, dw, N);
-    if (db) sum_parts_kernel<float><<<unsigned(cdiv(N, 32)), 256, 0, st>>>(part + N, parts, 2ll * N, db, N);
+    sum_parts<float>(part, parts, 2ll * N, dw, db, N, st);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

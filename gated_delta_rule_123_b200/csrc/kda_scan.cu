@@ -12,19 +12,22 @@
 // What bounds it: u, dt, z and y pass HBM once, but every (token, channel, state)
 // needs one exponential, and the special-function unit gives 16 a clock and SM.
 //
-// Layout.  A quad of lanes holds one channel, R = N / 4 states a lane; a block of
-// 128 threads holds 32 channels and walks its tokens in tiles of 32.  For each tile
-// a thread loads one token's 16-byte vector of 8 channels of u, dt and z while the
-// tile before is computed, turns them into (D, D u) pairs in shared memory, and
-// after the tile's recurrence finishes the same 8 outputs, so global memory is read
-// and written in whole vectors once.  Sums over n: four tokens of a quad are
-// reduced together by a transposing exchange (3 shuffles for 4 tokens), which
-// leaves each lane with one token's sum.
+// Layout.  A lane holds one channel with all its states, a warp 32 channels, and
+// warps are independent blocks.  So the step size, its decays, the sum over the states
+// and the gate of a (token, channel) stay in one lane, with no exchange between lanes;
+// the N states are N independent chains, which hide each other's latency; and B and C
+// are the same for the whole warp: one broadcast 16-byte read of shared memory serves
+// four states of 32 channels.  (Four or eight lanes to a channel, for more warps from
+// the same channels, measured 480 us at 8192 tokens x 4096 channels x 16 states where
+// this layout takes 365: the exchange and the per-lane copies of D and D u made the
+// shared-memory pipe and the instruction issue the bound.)  u, dt, z, B and C are
+// copied a tile of 16 tokens ahead into shared memory by cp.async.
 //
-// Few sequences do not fill the SMs, so the token axis is cut into segments: a
-// first pass runs all but the last one's recurrence from a zero state (no y) and
-// leaves the end state and sum(D) of each; since the decay over a segment is
+// Few sequences and channels do not fill the SMs, so the token axis is cut into
+// segments: a first pass runs all but the last one's recurrence from a zero state (no
+// y) and leaves the end state and sum(D) of each; since the decay over a segment is
 // exp(A sum(D)), the second pass starts each segment from the states before it.
+#include <stdlib.h>
 #include "kda_mixer.cuh"
 
 namespace kda {
@@ -35,8 +38,7 @@ using namespace mix;
 
 constexpr int kTT = 32;   // tokens of a tile
 constexpr int kCh = 32;   // channels of a block
-constexpr int kYP = 40;   // row pitch of the tile of sums: quads' four rows fall on different banks
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kYP = 40;   // row pitch of the backward pass's tiles of sums (a quad's four rows on different banks)
 
 struct SArgs {
     const void *u, *dt, *z, *Bm, *Cm, *dy;
@@ -116,12 +118,6 @@ __device__ __forceinline__ void load_states(VR<T, R>& r, const void* base, long 
     }
 }
 
-// 2^x on the special-function unit (relative error about 2^-22; below 2^-126 it gives 0).
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float step_size(float raw, int softplus) { return softplus ? softplusf(raw) : raw; }
 
 // R fp32 states of (row r of [..][N]) at n0; zero beyond N.
@@ -137,14 +133,17 @@ __device__ __forceinline__ void store_h(const float (&h)[R], float* p, int n0, i
         if (n0 + i < N) p[n0 + i] = h[i];
 }
 
-// v[j] of the quad's four lanes summed; lane q is left with the sum of v[q].
-__device__ __forceinline__ float quad_transpose_sum(const float (&v)[4], int q) {
-    const bool hi = q & 2, lo = q & 1;
-    float a0 = hi ? v[2] : v[0], a1 = hi ? v[3] : v[1];
-    a0 += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 2);
-    a1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 2);
-    const float k = lo ? a1 : a0;
-    return k + __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, 1);
+// v[j] summed over L neighbouring lanes; lane q of them is left with the sum of v[q].
+template <int L>
+__device__ __forceinline__ float lane_transpose_sum(float (&v)[L], int q) {
+#pragma unroll
+    for (int s = L / 2; s >= 1; s /= 2)
+#pragma unroll
+        for (int i = 0; i < s; ++i) {
+            const float keep = q & s ? v[s + i] : v[i], give = q & s ? v[i] : v[s + i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, s);
+        }
+    return v[0];
 }
 
 // What a block works on: segment s of row b, channels d0 .. of group g.
@@ -184,153 +183,266 @@ __device__ __forceinline__ void state_before(float (&h)[R], const SArgs& a, cons
     }
 }
 
-// kOut false: the map of a segment (end state from zero, sum of D).  kOut true: outputs.
-template <typename T, int R, bool kVec, bool kOut>
-__global__ void __launch_bounds__(128) fwd_kernel(const SArgs a, bool bc_vec) {
-    __shared__ __align__(16) float2 sdu[2][kTT][kCh];
-    __shared__ __align__(16) float sb[2][kTT][4 * R];
-    __shared__ __align__(16) float sc[kOut ? 2 : 1][kOut ? kTT : 1][4 * R];
-    __shared__ __align__(16) float sy[kOut ? kTT : 1][kYP];
-    __shared__ float sbias[kCh], sskip[kCh];
-    __shared__ int sfirst[kTT], slast[kTT];
+constexpr int kFT = 16;  // tokens of a tile in the forward pass
 
-    const int tid = threadIdx.x, q = tid & 3, c = tid >> 2;  // quad lane and channel; also: vector and token
+template <typename T, int NP, bool kOut>
+struct FwdSmem {
+    // this tile's and the next one's inputs
+    T u[2][kFT][kCh], dt[2][kFT][kCh], z[kOut ? 2 : 1][kOut ? kFT : 1][kCh];
+    T b[2][kFT][NP], c[kOut ? 2 : 1][kOut ? kFT : 1][NP];
+    float bc[kFT][kOut ? 2 * NP : NP];  // this tile's B, then C, as fp32
+    int first[kFT], last[kFT];
+};
+
+// A tile of 32 channels of rows [tt, tt + n) into shared memory; columns past `valid` are
+// left as they were (whole vectors) or 0.
+template <typename T, bool kVec, int kTok>
+__device__ __forceinline__ void stage_tile(T (&dst)[kTok][kCh], const void* base, long long tt, int n, long long ld, int d0,
+                                           int valid, int lane) {
+    const T* p = static_cast<const T*>(base) + tt * ld + d0;
+    if constexpr (kVec) {
+        constexpr int kE = 16 / sizeof(T), kRow = kCh / kE;  // vectors of a row
+#pragma unroll
+        for (int i = 0; i < kTok * kRow / 32; ++i) {
+            const int k = (lane + 32 * i) / kRow, v = (lane + 32 * i) % kRow;
+            if (k < n && v * kE < valid) cp_async<16>(&dst[k][v * kE], p + k * ld + v * kE);
+        }
+    } else {
+        T r[kTok];
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) r[k] = k < n && lane < valid ? p[k * ld + lane] : from_f32<T>(0.f);
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) dst[k][lane] = r[k];
+    }
+}
+// The same for a group's NP states of B or C (states past N are 0).
+template <typename T, int NP, int kTok>
+__device__ __forceinline__ void stage_bc(T (&dst)[kTok][NP], const void* base, long long tt, int n, long long ld, long long off,
+                                         int N, bool vec, int lane) {
+    const T* p = static_cast<const T*>(base) + tt * ld + off;
+    if (vec) {
+        constexpr int kE = 16 / sizeof(T), kRow = NP / kE;
+#pragma unroll
+        for (int i = 0; i < (kTok * kRow + 31) / 32; ++i) {
+            const int k = (lane + 32 * i) / kRow, v = (lane + 32 * i) % kRow;
+            if (k < n) cp_async<16>(&dst[k][v * kE], p + k * ld + v * kE);
+        }
+    } else {
+#pragma unroll 4
+        for (int i = lane; i < kTok * NP; i += 32) {
+            const int k = i / NP, m = i % NP;
+            dst[k][m] = k < n && m < N ? p[k * ld + m] : from_f32<T>(0.f);
+        }
+    }
+}
+
+// B (and C) of a tile as fp32, 8 (bf16) or 4 values a step.
+template <typename T, int NP, int kW, int kTok>
+__device__ __forceinline__ void widen_rows(float (&dst)[kTok][kW], int col, const T (&src)[kTok][NP], int lane) {
+    constexpr int kE = 16 / sizeof(T), kAll = kTok * NP / kE;
+#pragma unroll
+    for (int i = 0; i < (kAll + 31) / 32; ++i) {
+        const int e = (lane + 32 * i) * kE, k = e / NP, m = e % NP;
+        if (kAll % 32 == 0 || k < kTok) {
+            float f[kE];
+            unpack16(*reinterpret_cast<const uint4*>(&src[k][m]), f, T());
+#pragma unroll
+            for (int u = 0; u < kE; u += 4)
+                *reinterpret_cast<float4*>(&dst[k][col + m + u]) = make_float4(f[u], f[u + 1], f[u + 2], f[u + 3]);
+        }
+    }
+}
+
+// All NP states of a channel, in pairs; states past N are 0.
+template <int NP>
+__device__ __forceinline__ void load_pairs(f2 (&h)[NP / 2], const float* p, int N) {
+    if (N == NP && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i) {
+            const float4 v = reinterpret_cast<const float4*>(p)[i];
+            h[2 * i] = pk(v.x, v.y);
+            h[2 * i + 1] = pk(v.z, v.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) h[i] = pk(2 * i < N ? p[2 * i] : 0.f, 2 * i + 1 < N ? p[2 * i + 1] : 0.f);
+    }
+}
+template <int NP>
+__device__ __forceinline__ void store_pairs(const f2 (&h)[NP / 2], float* p, int N) {
+    if (N == NP && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i) {
+            float4 v;
+            upk(h[2 * i], v.x, v.y);
+            upk(h[2 * i + 1], v.z, v.w);
+            reinterpret_cast<float4*>(p)[i] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) {
+            float a, b;
+            upk(h[i], a, b);
+            if (2 * i < N) p[2 * i] = a;
+            if (2 * i + 1 < N) p[2 * i + 1] = b;
+        }
+    }
+}
+
+// kOut false: the map of a segment (end state from zero, sum of D).  kOut true: outputs.
+template <typename T, int NP, bool kVec, bool kOut>
+__global__ void __launch_bounds__(32, 20) fwd_kernel(const SArgs a, bool bc_vec) {
+    constexpr int kP = NP / 2;
+    __shared__ __align__(128) FwdSmem<T, NP, kOut> sm;
+    const int lane = threadIdx.x;
     Place p = place(a);
-    const int d = p.d0 + c, n0 = q * R;
-    const bool live = d < p.dend;
+    const int d = p.d0 + lane, valid = p.dend - p.d0;
+    const bool live = lane < valid;
     if (!kOut) {  // only what the segment after this one needs
         if (p.s == a.S - 1) return;
         const int n = seq_of(a.cu, a.nseq, a.seq_len, int(p.t1 - 1));
         const long long sbeg = seq_begin(a.cu, a.seq_len, n);
         if (sbeg > p.t0) p.t0 = sbeg;
     }
-    float A2[R], h[R], dsum = 0.f;
+    f2 A2[kP], h[kP];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        A2[r] = live && n0 + r < a.N ? a.A[(size_t)d * a.N + n0 + r] * kLog2e : 0.f;
-        h[r] = 0.f;
+    for (int i = 0; i < kP; ++i) A2[i] = h[i] = 0ull;
+    if (live) {
+        load_pairs<NP>(A2, a.A + (size_t)d * a.N, a.N);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) A2[i] = mul2(A2[i], dup2(kL2e));
     }
-    if (tid < kCh) {
-        const int e = p.d0 + tid;
-        sbias[tid] = a.bias && e < p.dend ? a.bias[e] : 0.f;
-        sskip[tid] = a.skip && e < p.dend ? a.skip[e] : 0.f;
-    }
+    const float bias = a.bias && live ? a.bias[d] : 0.f, skip = kOut && a.skip && live ? a.skip[d] : 0.f;
+    const size_t at = (size_t)d * a.N, row = (size_t)a.D * a.N;  // of a [channels][N] state
     if (kOut && a.hT)  // empty sequences hand their initial state on
         for (int n = blockIdx.y; n < a.nseq; n += gridDim.y)
             if (live && seq_begin(a.cu, a.seq_len, n) == seq_begin(a.cu, a.seq_len, n + 1)) {
-                float e[R];
+                f2 e[kP];
 #pragma unroll
-                for (int r = 0; r < R; ++r) e[r] = 0.f;
-                if (a.h0) load_h<R>(e, a.h0 + ((size_t)n * a.D + d) * a.N, n0, a.N);
-                store_h<R>(e, a.hT + ((size_t)n * a.D + d) * a.N, n0, a.N);
+                for (int i = 0; i < kP; ++i) e[i] = 0ull;
+                if (a.h0) load_pairs<NP>(e, a.h0 + n * row + at, a.N);
+                store_pairs<NP>(e, a.hT + n * row + at, a.N);
             }
     if (p.t0 >= p.t1) return;
     int n = seq_of(a.cu, a.nseq, a.seq_len, int(p.t0));
     long long s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
-    if (live) {
-        if (kOut && s_beg < p.t0) state_before<R>(h, a, p, s_beg, d, n0, A2);
-        else if (!kOut && s_beg == p.t0 && a.h0) load_h<R>(h, a.h0 + ((size_t)n * a.D + d) * a.N, n0, a.N);
+    if (live && kOut && s_beg < p.t0) {
+        // the state at t0: the map of the segment that holds the sequence's start begins
+        // with that sequence's initial state; the maps after it are applied in order
+        const long long base = (long long)p.b * a.S;
+        const int sb = int((s_beg - p.row0) / a.L);
+        load_pairs<NP>(h, a.seg_h + (base + sb) * row + at, a.N);
+        for (int i = sb + 1; i < p.s; ++i) {
+            f2 e[kP];
+            load_pairs<NP>(e, a.seg_h + (base + i) * row + at, a.N);
+            const f2 sd = dup2(a.seg_d[(base + i) * a.D + d]);
+#pragma unroll
+            for (int k = 0; k < kP; ++k) {
+                float x0, x1;
+                upk(mul2(A2[k], sd), x0, x1);
+                h[k] = fma2(pk(ex2(x0), ex2(x1)), h[k], e[k]);
+            }
+        }
+    } else if (live && !kOut && s_beg == p.t0 && a.h0) {
+        load_pairs<NP>(h, a.h0 + n * row + at, a.N);
     }
 
-    // this thread's part of a tile: token c of the tile, channels d0 + 8 q .., states n0 ..
-    const int dv = p.d0 + 8 * q, valid = p.dend - dv;
-    V8<T> ru, rd, rz;
-    VR<T, R> rb, rc;
-    auto request = [&](long long tt) {
-        const long long t = tt + c;
-        if (t < p.t1) {
-            load8<T, kVec>(ru, a.u, t, a.ldu, dv, valid);
-            load8<T, kVec>(rd, a.dt, t, a.lddt, dv, valid);
-            load_states<T, R>(rb, a.Bm, t * a.ldb + (long long)p.g * a.N, n0, a.N, bc_vec);
-            if constexpr (kOut) {
-                load_states<T, R>(rc, a.Cm, t * a.ldc + (long long)p.g * a.N, n0, a.N, bc_vec);
-                if (a.z) load8<T, kVec>(rz, a.z, t, a.ldz, dv, valid);
-            }
-        }
-    };
-    request(p.t0);
-    __syncthreads();  // sbias and sskip
+    float dsum = 0.f;
     int buf = 0;
-    for (long long tt = p.t0; tt < p.t1; tt += kTT, buf ^= 1) {
-        const long long t = tt + c;
-        const bool here = t < p.t1;
-        // sequence starts and ends inside the tile
-        const bool edges = kOut && !(s_beg < tt && s_end > tt + kTT);
-        if (edges && q == 0) {
-            int f = -1, l = -1;
-            if (here) {
-                const int m = seq_of(a.cu, a.nseq, a.seq_len, int(t));
-                if (seq_begin(a.cu, a.seq_len, m) == t) f = m;
-                if (seq_begin(a.cu, a.seq_len, m + 1) == t + 1) l = m;
-            }
-            sfirst[c] = f;
-            slast[c] = l;
-        }
-        float u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // tokens past the end: D = 0, the state stays
-            u[i] = here ? to_f32<T>(ru.v[i]) : 0.f;
-            const float D = here ? step_size(to_f32<T>(rd.v[i]) + sbias[8 * q + i], a.softplus) : 0.f;
-            sdu[buf][c][8 * q + i] = make_float2(D, D * u[i]);
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            sb[buf][c][n0 + r] = here ? to_f32<T>(rb.v[r]) : 0.f;
-            if constexpr (kOut) sc[buf][c][n0 + r] = here ? to_f32<T>(rc.v[r]) : 0.f;
-        }
-        V8<T> z = rz;
-        __syncthreads();
-        if (tt + kTT < p.t1) request(tt + kTT);
-        const int steps = int(p.t1 - tt < kTT ? p.t1 - tt : kTT);
-#pragma unroll 2
-        for (int j4 = 0; j4 < steps; j4 += 4) {
-            float acc[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = j4 + j;
-                if (edges && sfirst[k] >= 0) {
-#pragma unroll
-                    for (int r = 0; r < R; ++r) h[r] = 0.f;
-                    if (a.h0 && live) load_h<R>(h, a.h0 + ((size_t)sfirst[k] * a.D + d) * a.N, n0, a.N);
-                }
-                const float2 du = sdu[buf][k][c];
-                acc[j] = 0.f;
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    h[r] = ex2(du.x * A2[r]) * h[r] + du.y * sb[buf][k][n0 + r];
-                    if constexpr (kOut) acc[j] += h[r] * sc[buf][k][n0 + r];
-                }
-                if (!kOut) dsum += du.x;
-                if (edges && slast[k] >= 0 && a.hT && live)
-                    store_h<R>(h, a.hT + ((size_t)slast[k] * a.D + d) * a.N, n0, a.N);
-            }
-            if constexpr (kOut) sy[j4 + q][c] = quad_transpose_sum(acc, q);
-        }
+    auto request = [&](long long tt, int w) {
+        const int m = int(p.t1 - tt < kFT ? p.t1 - tt : kFT);
+        stage_tile<T, kVec>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
+        stage_tile<T, kVec>(sm.dt[w], a.dt, tt, m, a.lddt, p.d0, valid, lane);
+        stage_bc<T, NP>(sm.b[w], a.Bm, tt, m, a.ldb, (long long)p.g * a.N, a.N, bc_vec, lane);
         if constexpr (kOut) {
-            __syncthreads();
-            if (here) {
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    o[i] = sy[c][8 * q + i] + sskip[8 * q + i] * u[i];
-                    if (a.z) {
-                        const float g = to_f32<T>(z.v[i]);
-                        o[i] *= __fdividef(g, 1.f + __expf(-g));
-                    }
-                }
-                store8<T, kVec>(a.y, t, a.ldy, dv, valid, o);
+            stage_bc<T, NP>(sm.c[w], a.Cm, tt, m, a.ldc, (long long)p.g * a.N, a.N, bc_vec, lane);
+            if (a.z) stage_tile<T, kVec>(sm.z[w], a.z, tt, m, a.ldz, p.d0, valid, lane);
+        }
+        cp_async_commit();
+    };
+    request(p.t0, 0);
+    for (long long tt = p.t0; tt < p.t1; tt += kFT, buf ^= 1) {
+        const int steps = int(p.t1 - tt < kFT ? p.t1 - tt : kFT);
+        // sequence starts and ends inside the tile
+        const bool edges = kOut && !(s_beg < tt && s_end > tt + kFT);
+        if (edges && lane < kFT) {
+            int f = -1, l = -1;
+            if (lane < steps) {
+                const int m = seq_of(a.cu, a.nseq, a.seq_len, int(tt + lane));
+                if (seq_begin(a.cu, a.seq_len, m) == tt + lane) f = m;
+                if (seq_begin(a.cu, a.seq_len, m + 1) == tt + lane + 1) l = m;
             }
-            if (s_end <= tt + kTT && tt + kTT < p.t1) {
-                n = seq_of(a.cu, a.nseq, a.seq_len, int(tt + kTT));
-                s_beg = seq_begin(a.cu, a.seq_len, n);
-                s_end = seq_begin(a.cu, a.seq_len, n + 1);
+            sm.first[lane] = f;
+            sm.last[lane] = l;
+        }
+        cp_async_wait0();
+        __syncwarp();
+        widen_rows<T, NP>(sm.bc, 0, sm.b[buf], lane);
+        if constexpr (kOut) widen_rows<T, NP>(sm.bc, NP, sm.c[buf], lane);
+        __syncwarp();
+        if (tt + kFT < p.t1) request(tt + kFT, buf ^ 1);
+        T* yp = kOut ? static_cast<T*>(a.y) + tt * a.ldy + d : nullptr;
+        auto token = [&](int k) {
+            float D = to_f32<T>(sm.dt[buf][k][lane]) + bias;
+            if (a.softplus) D = softplus_poly(D);
+            const float u = to_f32<T>(sm.u[buf][k][lane]);
+            const f2 D2 = dup2(D), w2 = dup2(D * u);
+            f2 s[2] = {0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < kP; i += 2) {
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&sm.bc[k][2 * i]);
+                float x0, x1, x2, x3;
+                upk(mul2(D2, A2[i]), x0, x1);
+                upk(mul2(D2, A2[i + 1]), x2, x3);
+                h[i] = fma2(pk(ex2(x0), ex2(x1)), h[i], mul2(w2, b.x));
+                h[i + 1] = fma2(pk(ex2(x2), ex2(x3)), h[i + 1], mul2(w2, b.y));
+                if constexpr (kOut) {
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&sm.bc[k][NP + 2 * i]);
+                    s[0] = fma2(h[i], c.x, s[0]);
+                    s[1] = fma2(h[i + 1], c.y, s[1]);
+                }
+            }
+            if constexpr (kOut) {
+                const f2 t = add2(s[0], s[1]);
+                float y = (lo2(t) + hi2(t)) + skip * u;
+                if (a.z) y *= siluf(to_f32<T>(sm.z[buf][k][lane]));
+                if (live) yp[k * a.ldy] = from_f32<T>(y);
+            } else {
+                dsum += D;
+            }
+        };
+        if (!edges) {  // (tests for edges between the tokens would keep their loads and exponentials from overlapping)
+            int k = 0;
+#pragma unroll 1
+            for (; k + 4 <= steps; k += 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) token(k + j);
+            }
+#pragma unroll 1
+            for (; k < steps; ++k) token(k);
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k) {
+                if (sm.first[k] >= 0) {
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) h[i] = 0ull;
+                    if (a.h0 && live) load_pairs<NP>(h, a.h0 + sm.first[k] * row + at, a.N);
+                }
+                token(k);
+                if (sm.last[k] >= 0 && a.hT && live) store_pairs<NP>(h, a.hT + sm.last[k] * row + at, a.N);
             }
         }
+        if (kOut && s_end <= tt + kFT && tt + kFT < p.t1) {
+            n = seq_of(a.cu, a.nseq, a.seq_len, int(tt + kFT));
+            s_beg = seq_begin(a.cu, a.seq_len, n);
+            s_end = seq_begin(a.cu, a.seq_len, n + 1);
+        }
+        __syncwarp();
     }
     if (!kOut && live) {
         const long long i = (long long)p.b * a.S + p.s;
-        store_h<R>(h, a.seg_h + (i * a.D + d) * a.N, n0, a.N);
-        if (q == 0) a.seg_d[i * a.D + d] = dsum;
+        store_pairs<NP>(h, a.seg_h + i * row + at, a.N);
+        a.seg_d[i * a.D + d] = dsum;
     }
 }
 
@@ -369,7 +481,7 @@ __global__ void __launch_bounds__(256) step_kernel(const SArgs a, float* __restr
     for (int r = 0; r < R; ++r) {
         const bool in = kFull || n0 + r < a.N;
         const float Bv = in ? to_f32<T>(Bp[n0 + r]) : 0.f, Cv = in ? to_f32<T>(Cp[n0 + r]) : 0.f;
-        h[r] = ex2(D * A[r] * kLog2e) * h[r] + D * u * Bv;
+        h[r] = ex2(D * A[r] * kL2e) * h[r] + D * u * Bv;
         y += h[r] * Cv;
     }
     y += __shfl_xor_sync(0xffffffffu, y, 1);
@@ -394,10 +506,10 @@ __global__ void __launch_bounds__(256) step_kernel(const SArgs a, float* __restr
 }
 
 // ---------------------------------------------------------------- host side
+// States per lane of the step and of the backward pass (4 lanes a channel).
 static int states_per_lane(int N) { return N <= 8 ? 2 : (N <= 16 ? 4 : 8); }
 
-// Segments: enough blocks for the SMs, from segments long enough to pay for the map
-// pass, in whole tiles.
+// How the tokens are cut: segments of L tokens, S per row.
 struct Cut {
     int rows, row_len, bpg, L, S;
 };
@@ -406,10 +518,14 @@ static Cut fwd_cut(int B, int T, int D, int G, bool packed) {
     c.rows = packed ? 1 : B;
     c.row_len = T;
     c.bpg = int(cdiv(D / G, kCh));
-    const long long blocks = (long long)c.rows * G * c.bpg;
-    const long long want = (long long)device_sm_count() * 4;
-    long long S = blocks >= device_sm_count() ? 1 : cdiv(want, blocks);
-    const long long most = T / 256 < 32 ? T / 256 : 32;
+    // Unsegmented, 512 / 1024 warps take 450 / 300 us where segments take 360 (8192 x 4096
+    // x 16); with segments, 28 warps an SM measured best (14: 430 us, 56: 370 us).
+    const long long warps = (long long)c.rows * G * c.bpg, sms = device_sm_count();
+    long long S = warps >= 5 * sms ? 1 : cdiv(28 * sms, warps);
+#ifdef KDA_SCAN_TUNE
+    if (getenv("KDA_S")) S = atoi(getenv("KDA_S"));
+#endif
+    const long long most = T / 64 < 64 ? T / 64 : 64;
     if (S > most) S = most;
     if (S < 1) S = 1;
     c.L = int(cdiv(cdiv(T, S), kTT) * kTT);
@@ -423,26 +539,34 @@ static bool vec8_ok(const SArgs& a, int es, const void* const* ptrs, const long 
         if (ptrs[i] && (!al16(ptrs[i]) || (lds[i] * es) % 16)) return false;
     return true;
 }
-// B and C in whole vectors of R states.
-static bool states_ok(const SArgs& a, int es, int R) {
-    const int bytes = R * es < 16 ? R * es : 16;
-    return a.N == 4 * R && reinterpret_cast<uintptr_t>(a.Bm) % bytes == 0 && reinterpret_cast<uintptr_t>(a.Cm) % bytes == 0 &&
+static int padded_states(int N) { return N <= 8 ? 8 : (N <= 16 ? 16 : 32); }
+// B and C by 16-byte vectors: N is what a lane is padded to, and every group's row is aligned.
+static bool bc_whole(const SArgs& a, int es) {
+    return a.N == padded_states(a.N) && al16(a.Bm) && al16(a.Cm) && (a.ldb * es) % 16 == 0 && (a.ldc * es) % 16 == 0;
+}
+// B and C in whole vectors of n states.
+static bool states_ok(const SArgs& a, int es, int n) {
+    const int bytes = n * es < 16 ? n * es : 16;
+    return a.N == 4 * n && reinterpret_cast<uintptr_t>(a.Bm) % bytes == 0 && reinterpret_cast<uintptr_t>(a.Cm) % bytes == 0 &&
            (a.ldb * es) % bytes == 0 && (a.ldc * es) % bytes == 0;
 }
 
-template <typename T, int R>
+template <typename T, int NP, bool kVec>
+int fwd_run(const SArgs& a, bool bc, cudaStream_t st) {
+    const dim3 grid(a.G * a.bpg, a.rows * a.S);
+    if (a.S > 1) fwd_kernel<T, NP, kVec, false><<<grid, 32, 0, st>>>(a, bc);
+    fwd_kernel<T, NP, kVec, true><<<grid, 32, 0, st>>>(a, bc);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+template <typename T>
 int fwd(const SArgs& a, cudaStream_t st) {
     const void* ptrs[] = {a.u, a.dt, a.z, a.y};
     const long long lds[] = {a.ldu, a.lddt, a.ldz, a.ldy};
-    const bool vec = vec8_ok(a, sizeof(T), ptrs, lds, 4), bc = states_ok(a, sizeof(T), R);
-    const dim3 grid(a.G * a.bpg, a.rows * a.S);
-    if (a.S > 1) {
-        if (vec) fwd_kernel<T, R, true, false><<<grid, 128, 0, st>>>(a, bc);
-        else fwd_kernel<T, R, false, false><<<grid, 128, 0, st>>>(a, bc);
-    }
-    if (vec) fwd_kernel<T, R, true, true><<<grid, 128, 0, st>>>(a, bc);
-    else fwd_kernel<T, R, false, true><<<grid, 128, 0, st>>>(a, bc);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const bool vec = vec8_ok(a, sizeof(T), ptrs, lds, 4), bc = bc_whole(a, sizeof(T));
+    if (a.N <= 8) return vec ? fwd_run<T, 8, true>(a, bc, st) : fwd_run<T, 8, false>(a, bc, st);
+    if (a.N <= 16) return vec ? fwd_run<T, 16, true>(a, bc, st) : fwd_run<T, 16, false>(a, bc, st);
+    return vec ? fwd_run<T, 32, true>(a, bc, st) : fwd_run<T, 32, false>(a, bc, st);
 }
 
 template <typename T, int R>
@@ -477,18 +601,41 @@ static void scan_cut_args(scan::SArgs& a, const scan::Cut& c) {
     a.S = c.S;
 }
 
-size_t selective_scan_fwd_workspace_bytes(int B, int T, int D, int G, int N, bool packed) {
-    const scan::Cut c = scan::fwd_cut(B, T, D, G, packed);
-    if (c.S <= 1) return 0;
-    return mix::up256(size_t(c.rows) * c.S * D * N * 4) + mix::up256(size_t(c.rows) * c.S * D * 4);
+// Workspace of a segmented call: the segments' end states and sums, and a copy of the
+// initial states for a call that updates them in place (one segment's block writes a
+// sequence's final state while another's may still have to read its initial one).
+struct ScanFwdPlan {
+    scan::Cut c;
+    size_t off_d, off_h0, total;
+};
+static ScanFwdPlan scan_fwd_plan(int B, int T, int D, int G, int N, int num_seqs) {
+    ScanFwdPlan p{};
+    p.c = scan::fwd_cut(B, T, D, G, num_seqs > 0);
+    if (p.c.S <= 1) return p;
+    const size_t segs = size_t(p.c.rows) * p.c.S, nseq = num_seqs > 0 ? num_seqs : B;
+    p.off_d = mix::up256(segs * D * N * 4);
+    p.off_h0 = p.off_d + mix::up256(segs * D * 4);
+    p.total = p.off_h0 + mix::up256(nseq * D * N * 4);
+    return p;
+}
+size_t selective_scan_fwd_workspace_bytes(int B, int T, int D, int G, int N, int num_seqs) {
+    return scan_fwd_plan(B, T, D, G, N, num_seqs).total;
 }
 
 int launch_selective_scan_fwd(scan::SArgs a, int B, int tokens, int dtype, void* ws, cudaStream_t st) {
-    const scan::Cut c = scan::fwd_cut(B, tokens, a.D, a.G, a.cu != nullptr);
-    scan_cut_args(a, c);
-    a.seg_h = static_cast<float*>(ws);
-    a.seg_d = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + mix::up256(size_t(c.rows) * c.S * a.D * a.N * 4));
-    KDA_SCAN_DISPATCH(a.N, (scan::fwd<T, R>(a, st)))
+    const ScanFwdPlan p = scan_fwd_plan(B, tokens, a.D, a.G, a.N, a.cu ? a.nseq : 0);
+    scan_cut_args(a, p.c);
+    if (p.c.S > 1) {
+        uint8_t* b = static_cast<uint8_t*>(ws);
+        a.seg_h = reinterpret_cast<float*>(b);
+        a.seg_d = reinterpret_cast<float*>(b + p.off_d);
+        if (a.h0 && a.h0 == a.hT) {
+            if (cudaMemcpyAsync(b + p.off_h0, a.h0, size_t(a.nseq) * a.D * a.N * 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+                return KDA_ERR_CUDA;
+            a.h0 = reinterpret_cast<const float*>(b + p.off_h0);
+        }
+    }
+    return dtype == KDA_BF16 ? scan::fwd<__nv_bfloat16>(a, st) : scan::fwd<float>(a, st);
 }
 
 int launch_selective_scan_step(scan::SArgs a, float* state, int dtype, cudaStream_t st) {

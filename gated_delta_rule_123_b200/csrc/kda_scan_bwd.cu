@@ -9,20 +9,23 @@
 //   dDskip = sum_t p_t u_t       dz_t = dy_t (sum_n C_t h_t + Dskip u_t) SiLU'(z_t)     dh_0 = a_1 g_1
 //
 // States are needed in reverse order and are too many to keep, so a first pass
-// writes the state before every KC = 32 / R tokens, counted from a zero state at
-// its segment's start, with the sum of D up to there: the decay from the segment's
-// start to that token is exp(A sum(D)), so a checkpoint is completed by adding that
-// times the segment's incoming state.  The same pass accumulates the reverse map
-// of the segment, G = sum_t (a_1 .. a_t) C_t p_t: the gradient of the incoming
-// state is G + exp(A sum(D)) times the gradient of the state at its end.  So both
-// directions of the recurrence cross segments by a few operations per state, and
-// the second pass runs every segment on its own: per run of KC tokens it computes
-// the states forward from the checkpoint into registers, then walks back.
+// writes the state before every few tokens, counted from a zero state at its
+// segment's start, with the sum of D up to there: the decay from the segment's start
+// to that token is exp(A sum(D)), so a checkpoint is completed by adding that times
+// the segment's incoming state.  The same pass accumulates the reverse map of the
+// segment, G = sum_t (a_1 .. a_t) C_t p_t: the gradient of the incoming state is G +
+// exp(A sum(D)) times the gradient of the state at its end.  So both directions of
+// the recurrence cross segments by a few operations per state, and the second pass
+// runs every segment on its own: per run of KC tokens it computes the decays and
+// states forward from the checkpoint into registers, then walks back.
 //
-// The sums over n of a channel are sums over a quad of lanes (four tokens at a
-// time); the sums over the channels for dB and dC are sums over the eight quads of
-// a warp by a halving exchange, then over the warps and blocks in a fixed order:
-// every result is the same on every run.
+// Layout as in the forward pass, a lane per channel, so every sum over the states and
+// every sum over the tokens (dA, dDskip, dbias) stays in a lane.  The sums over the
+// channels for dB and dC are the only exchange; they go through shared memory, then
+// over the blocks in a fixed order: every result is the same on every run.  Bound by
+// the latency of 8 warps an SM: the registers hold KC tokens' decays and states.
+// Measured at 2 x 2047 tokens, 2048 channels, 16 states: 93 us the first pass, 280 us
+// the second (a quad of lanes to a channel: 164 and 633 us).
 #include "kda_mixer.cuh"
 
 namespace kda {
@@ -43,116 +46,483 @@ __device__ __forceinline__ void edge_flags(const SArgs& a, long long t, bool her
     }
 }
 
-template <typename T, int R, bool kVec>
-__global__ void __launch_bounds__(128) bwd_map_kernel(const SArgs a, bool bc_vec) {
-    constexpr int KC = 32 / R;
-    __shared__ __align__(16) float2 sdu[2][kTT][kCh];
-    __shared__ float sp[2][kTT][kCh + 8];
-    __shared__ __align__(16) float sb[2][kTT][4 * R], sc[2][kTT][4 * R];
-    __shared__ float sbias[kCh];
-    __shared__ int sfirst[2][kTT], slast[2][kTT];
-    const int tid = threadIdx.x, q = tid & 3, c = tid >> 2;
+// Tokens between two checkpoints of a channel padded to NP states: as many as the
+// second pass can hold in registers (decays and states of every token).
+__host__ __device__ constexpr int ckpt_tokens(int NP) { return NP <= 8 ? 8 : 4; }
+
+template <typename T, int NP>
+struct MapSmem {
+    T u[2][kFT][kCh], dt[2][kFT][kCh], z[2][kFT][kCh], dy[2][kFT][kCh];
+    T b[2][kFT][NP], c[2][kFT][NP];
+    float bc[kFT][2 * NP];
+    int first[kFT], last[kFT];
+};
+
+// The first pass, in the forward pass's layout (a lane holds a channel): states before
+// every KC tokens from a zero state, the sums of D up to there, the segment's end state
+// and its reverse map.
+template <typename T, int NP, bool kVec>
+__global__ void __launch_bounds__(32) bwd_map_kernel(const SArgs a, bool bc_vec) {
+    constexpr int kP = NP / 2, KC = ckpt_tokens(NP);
+    __shared__ __align__(128) MapSmem<T, NP> sm;
+    const int lane = threadIdx.x;
     const Place p = place(a);
     if (p.t0 >= p.t1) return;
-    const int d = p.d0 + c, n0 = q * R;
-    const bool live = d < p.dend;
-    float A2[R], h[R], P[R], G[R], dsum = 0.f;
-    bool open = true;  // no sequence has ended in the segment yet: later tokens do not see the incoming state
+    const int d = p.d0 + lane, valid = p.dend - p.d0;
+    const bool live = lane < valid;
+    f2 A2[kP], h[kP], P[kP], G[kP];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        A2[r] = live && n0 + r < a.N ? a.A[(size_t)d * a.N + n0 + r] * kLog2e : 0.f;
-        h[r] = G[r] = 0.f;
-        P[r] = 1.f;
+    for (int i = 0; i < kP; ++i) {
+        A2[i] = h[i] = G[i] = 0ull;
+        P[i] = dup2(1.f);
     }
-    if (tid < kCh) sbias[tid] = a.bias && p.d0 + tid < p.dend ? a.bias[p.d0 + tid] : 0.f;
-    const int dv = p.d0 + 8 * q, valid = p.dend - dv;
-    V8<T> ru, rd, rz, ry;
-    VR<T, R> rb, rc;
-    auto request = [&](long long tt) {
-        const long long t = tt + c;
-        if (t < p.t1) {
-            load8<T, kVec>(ru, a.u, t, a.ldu, dv, valid);
-            load8<T, kVec>(rd, a.dt, t, a.lddt, dv, valid);
-            load8<T, kVec>(ry, a.dy, t, a.lddy, dv, valid);
-            if (a.z) load8<T, kVec>(rz, a.z, t, a.ldz, dv, valid);
-            load_states<T, R>(rb, a.Bm, t * a.ldb + (long long)p.g * a.N, n0, a.N, bc_vec);
-            load_states<T, R>(rc, a.Cm, t * a.ldc + (long long)p.g * a.N, n0, a.N, bc_vec);
-        }
+    if (live) {
+        load_pairs<NP>(A2, a.A + (size_t)d * a.N, a.N);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) A2[i] = mul2(A2[i], dup2(kL2e));
+    }
+    const float bias = a.bias && live ? a.bias[d] : 0.f;
+    const size_t at = (size_t)d * a.N, row = (size_t)a.D * a.N;
+    bool open = true;  // no sequence has ended in the segment yet: later tokens do not see the incoming state
+    float dsum = 0.f;
+    int n = seq_of(a.cu, a.nseq, a.seq_len, int(p.t0));
+    long long s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
+    auto request = [&](long long tt, int w) {
+        const int m = int(p.t1 - tt < kFT ? p.t1 - tt : kFT);
+        stage_tile<T, kVec>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
+        stage_tile<T, kVec>(sm.dt[w], a.dt, tt, m, a.lddt, p.d0, valid, lane);
+        stage_tile<T, kVec>(sm.dy[w], a.dy, tt, m, a.lddy, p.d0, valid, lane);
+        if (a.z) stage_tile<T, kVec>(sm.z[w], a.z, tt, m, a.ldz, p.d0, valid, lane);
+        stage_bc<T, NP>(sm.b[w], a.Bm, tt, m, a.ldb, (long long)p.g * a.N, a.N, bc_vec, lane);
+        stage_bc<T, NP>(sm.c[w], a.Cm, tt, m, a.ldc, (long long)p.g * a.N, a.N, bc_vec, lane);
+        cp_async_commit();
     };
-    request(p.t0);
-    __syncthreads();
+    request(p.t0, 0);
     const long long chunk0 = ((long long)p.b * a.S + p.s) * (a.L / KC);
     int buf = 0;
-    for (long long tt = p.t0; tt < p.t1; tt += kTT, buf ^= 1) {
-        const bool here = tt + c < p.t1;
-        int ef = -1, el = -1;
-        if (q == 0) {
-            edge_flags(a, tt + c, here, ef, el);
-            sfirst[buf][c] = ef;
-            slast[buf][c] = el;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float u = here ? to_f32<T>(ru.v[i]) : 0.f;
-            const float D = here ? step_size(to_f32<T>(rd.v[i]) + sbias[8 * q + i], a.softplus) : 0.f;
-            float pv = here ? to_f32<T>(ry.v[i]) : 0.f;
-            if (a.z && here) {
-                const float z = to_f32<T>(rz.v[i]);
-                pv *= __fdividef(z, 1.f + __expf(-z));
-            }
-            sdu[buf][c][8 * q + i] = make_float2(D, D * u);
-            sp[buf][c][8 * q + i] = pv;
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            sb[buf][c][n0 + r] = here ? to_f32<T>(rb.v[r]) : 0.f;
-            sc[buf][c][n0 + r] = here ? to_f32<T>(rc.v[r]) : 0.f;
-        }
-        const bool edges = __syncthreads_or(ef >= 0 || el >= 0);
-        if (tt + kTT < p.t1) request(tt + kTT);
-        const int steps = int(p.t1 - tt < kTT ? p.t1 - tt : kTT);
-#pragma unroll 1
-        for (int k0 = 0; k0 < steps; k0 += KC) {
-            const long long ck = chunk0 + (tt - p.t0 + k0) / KC;
+    for (long long tt = p.t0; tt < p.t1; tt += kFT, buf ^= 1) {
+        const int steps = int(p.t1 - tt < kFT ? p.t1 - tt : kFT);
+        const bool edges = !(s_beg < tt && s_end > tt + kFT);
+        if (edges && lane < kFT) edge_flags(a, tt + lane, lane < steps, sm.first[lane], sm.last[lane]);
+        cp_async_wait0();
+        __syncwarp();
+        widen_rows<T, NP>(sm.bc, 0, sm.b[buf], lane);
+        widen_rows<T, NP>(sm.bc, NP, sm.c[buf], lane);
+        __syncwarp();
+        if (tt + kFT < p.t1) request(tt + kFT, buf ^ 1);
+        auto keep = [&](int k) {  // the checkpoint before token k
+            const long long ck = chunk0 + (tt - p.t0 + k) / KC;
             if (live) {
-                store_h<R>(h, a.ckpt + (ck * a.D + d) * a.N, n0, a.N);
-                if (q == 0) a.ckpt_d[ck * a.D + d] = dsum;
+                store_pairs<NP>(h, a.ckpt + (ck * a.D + d) * NP, NP);
+                a.ckpt_d[ck * a.D + d] = dsum;
             }
+        };
+        auto token = [&](int k, auto reverse) {
+            constexpr bool kOpen = decltype(reverse)::value;
+            float D = to_f32<T>(sm.dt[buf][k][lane]) + bias;
+            if (a.softplus) D = softplus_poly(D);
+            float pv = to_f32<T>(sm.dy[buf][k][lane]);
+            if (a.z) pv *= siluf(to_f32<T>(sm.z[buf][k][lane]));
+            const f2 D2 = dup2(D), w2 = dup2(D * to_f32<T>(sm.u[buf][k][lane])), p2 = dup2(pv);
 #pragma unroll
-            for (int j = 0; j < KC; ++j) {
-                const int k = k0 + j;
-                if (edges && sfirst[buf][k] >= 0) {
-#pragma unroll
-                    for (int r = 0; r < R; ++r) h[r] = 0.f;
-                    if (a.h0 && live) load_h<R>(h, a.h0 + ((size_t)sfirst[buf][k] * a.D + d) * a.N, n0, a.N);
+            for (int i = 0; i < kP; i += 2) {
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&sm.bc[k][2 * i]);
+                const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&sm.bc[k][NP + 2 * i]);
+                float x0, x1, x2, x3;
+                upk(mul2(D2, A2[i]), x0, x1);
+                upk(mul2(D2, A2[i + 1]), x2, x3);
+                const f2 e0 = pk(ex2(x0), ex2(x1)), e1 = pk(ex2(x2), ex2(x3));
+                h[i] = fma2(e0, h[i], mul2(w2, b.x));
+                h[i + 1] = fma2(e1, h[i + 1], mul2(w2, b.y));
+                if constexpr (kOpen) {
+                    P[i] = mul2(P[i], e0);
+                    P[i + 1] = mul2(P[i + 1], e1);
+                    G[i] = fma2(P[i], mul2(c.x, p2), G[i]);
+                    G[i + 1] = fma2(P[i + 1], mul2(c.y, p2), G[i + 1]);
                 }
-                const float2 du = sdu[buf][k][c];
-                const float pv = sp[buf][k][c];
+            }
+            dsum += D;
+        };
+        auto run = [&](auto reverse) {
+            int k = 0;
+#pragma unroll 1
+            for (; k + 4 <= steps; k += 4) {
+                if (k % KC == 0) keep(k);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float e = ex2(du.x * A2[r]);
-                    h[r] = e * h[r] + du.y * sb[buf][k][n0 + r];
-                    P[r] *= e;
-                    if (open) G[r] += P[r] * (sc[buf][k][n0 + r] * pv);
+                for (int j = 0; j < 4; ++j) token(k + j, reverse);
+            }
+            if (k < steps && k % KC == 0) keep(k);
+#pragma unroll 1
+            for (; k < steps; ++k) token(k, reverse);
+        };
+        if (!edges) {
+            if (open) run(std::true_type{});
+            else run(std::false_type{});
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k) {
+                if (k % KC == 0) keep(k);
+                if (sm.first[k] >= 0) {
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) h[i] = 0ull;
+                    if (a.h0 && live) load_pairs<NP>(h, a.h0 + sm.first[k] * row + at, a.N);
                 }
-                dsum += du.x;
-                if (edges && slast[buf][k] >= 0) {
+                if (open) token(k, std::true_type{});
+                else token(k, std::false_type{});
+                if (sm.last[k] >= 0) {
                     if (open && a.dhT && live) {
-                        float e[R];
-                        load_h<R>(e, a.dhT + ((size_t)slast[buf][k] * a.D + d) * a.N, n0, a.N);
+                        f2 e[kP];
+                        load_pairs<NP>(e, a.dhT + sm.last[k] * row + at, a.N);
 #pragma unroll
-                        for (int r = 0; r < R; ++r) G[r] += P[r] * e[r];
+                        for (int i = 0; i < kP; ++i) G[i] = fma2(P[i], e[i], G[i]);
                     }
                     open = false;
                 }
             }
         }
+        if (s_end <= tt + kFT && tt + kFT < p.t1) {
+            n = seq_of(a.cu, a.nseq, a.seq_len, int(tt + kFT));
+            s_beg = seq_begin(a.cu, a.seq_len, n);
+            s_end = seq_begin(a.cu, a.seq_len, n + 1);
+        }
+        __syncwarp();
     }
     if (live) {
         const long long i = (long long)p.b * a.S + p.s;
-        store_h<R>(h, a.seg_h + (i * a.D + d) * a.N, n0, a.N);
-        store_h<R>(G, a.seg_g + (i * a.D + d) * a.N, n0, a.N);
-        if (q == 0) a.seg_d[i * a.D + d] = dsum;
+        store_pairs<NP>(h, a.seg_h + i * row + at, a.N);
+        store_pairs<NP>(G, a.seg_g + i * row + at, a.N);
+        a.seg_d[i * a.D + d] = dsum;
+    }
+}
+
+// One value of 2 NP per lane and column, summed over the warp's lanes (channels): the
+// lanes write their rows to shared memory, a lane adds 4 columns of a part of the rows
+// and the parts are added by a halving exchange, which leaves 4 / halvings values with
+// a lane.  Rows of 2 NP + 4 floats: no bank twice, writing or reading.
+template <int NP>
+struct ChannelSum {
+    static constexpr int kCols = 2 * NP, kPitch = kCols + 4, kCG = kCols / 4, kRG = 32 / kCG;  // column and row groups
+    static constexpr int kLeft = kRG >= 4 ? 1 : 2;
+    float s[2][32][kPitch];
+};
+template <int NP>
+__device__ __forceinline__ void channel_sum_write(ChannelSum<NP>& cs, int buf, int lane, int col, f2 v0, f2 v1) {
+    ulonglong2 v;
+    v.x = v0;
+    v.y = v1;
+    *reinterpret_cast<ulonglong2*>(&cs.s[buf][lane][col]) = v;
+}
+// To be called after a __syncwarp; writes the sums to out[0 .. 2N) (dB, then dC).
+template <int NP>
+__device__ __forceinline__ void channel_sum_read(const ChannelSum<NP>& cs, int buf, int lane, float* out, int N) {
+    using C = ChannelSum<NP>;
+    const int cg = lane % C::kCG, rg = lane / C::kCG;
+    f2 a = 0ull, b = 0ull;
+#pragma unroll
+    for (int r = 0; r < 32 / C::kRG; ++r) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&cs.s[buf][rg * (32 / C::kRG) + r][cg * 4]);
+        a = add2(a, v.x);
+        b = add2(b, v.y);
+    }
+    float v[4];
+    upk(a, v[0], v[1]);
+    upk(b, v[2], v[3]);
+    int col = cg * 4;
+    {
+        const bool up = lane & 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float keep = up ? v[2 + i] : v[i], give = up ? v[i] : v[2 + i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+        }
+        col += up ? 2 : 0;
+    }
+    if constexpr (C::kRG >= 4) {
+        const bool up = lane & 8;
+        const float keep = up ? v[1] : v[0], give = up ? v[0] : v[1];
+        v[0] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+        col += up ? 1 : 0;
+    }
+    if constexpr (C::kRG >= 8) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 4);
+#pragma unroll
+    for (int i = 0; i < C::kLeft; ++i) {
+        const int c = col + i, n = c % NP;
+        if (n < N && (C::kRG < 8 || !(lane & 4))) out[(c / NP) * N + n] = v[i];
+    }
+}
+
+constexpr int kMT = 8;  // tokens of a tile in the second pass: its shared memory lets the registers bound the warps of an SM
+
+template <typename T, int NP>
+struct MainSmem {
+    static constexpr int kChunks = kMT / ckpt_tokens(NP);
+    T u[2][kMT][kCh], dt[2][kMT][kCh], z[2][kMT][kCh], dy[2][kMT][kCh];
+    T b[2][kMT][NP], c[2][kMT][NP];
+    float ck[2][kChunks][32 * NP];  // the tile's checkpoints, a lane's 16-byte vectors swizzled
+    float ckd[2][kChunks][32];
+    float bc[kMT][2 * NP];
+    float hin[32 * NP];  // the state that enters the segment, swizzled alike
+    ChannelSum<NP> sum;
+    int first[kMT], last[kMT];
+};
+// Place of vector i (4 states) of a lane's NP states: eight neighbouring lanes touch no bank twice.
+template <int NP>
+__device__ __forceinline__ int swz(int lane, int i) {
+    constexpr int kV = NP / 4;  // vectors of a lane: 2 or 4
+    return (lane * kV + (i ^ ((lane / (8 / kV)) & (kV - 1)))) * 4;
+}
+
+// The second pass for up to 16 states: a lane holds a channel.
+template <typename T, int NP, bool kVec>
+__global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
+    constexpr int kP = NP / 2, KC = ckpt_tokens(NP), kV = NP / 4;
+    using Smem = MainSmem<T, NP>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+    const int lane = threadIdx.x;
+    const Place p = place(a);
+    const int d = p.d0 + lane, valid = p.dend - p.d0;
+    const bool live = lane < valid;
+    const long long si = (long long)p.b * a.S + p.s;
+    const size_t at = (size_t)d * a.N, row = (size_t)a.D * a.N;
+    f2 A2[kP], g[kP], dA[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) A2[i] = g[i] = dA[i] = 0ull;
+    if (live) {
+        load_pairs<NP>(A2, a.A + (size_t)d * a.N, a.N);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) A2[i] = mul2(A2[i], dup2(kL2e));
+    }
+    const float bias = a.bias && live ? a.bias[d] : 0.f, skip = a.skip && live ? a.skip[d] : 0.f;
+    if (a.dh0)  // empty sequences hand the final state's gradient on
+        for (int n = blockIdx.y; n < a.nseq; n += gridDim.y)
+            if (live && seq_begin(a.cu, a.seq_len, n) == seq_begin(a.cu, a.seq_len, n + 1)) {
+                f2 e[kP];
+#pragma unroll
+                for (int i = 0; i < kP; ++i) e[i] = 0ull;
+                if (a.dhT) load_pairs<NP>(e, a.dhT + n * row + at, a.N);
+                store_pairs<NP>(e, a.dh0 + n * row + at, a.N);
+            }
+    if (p.t0 >= p.t1) return;
+    auto decay = [&](f2 A, f2 x) {
+        float x0, x1;
+        upk(mul2(A, x), x0, x1);
+        return pk(ex2(x0), ex2(x1));
+    };
+    // the state that enters the segment, and the gradient that enters at its end
+    const int nf = seq_of(a.cu, a.nseq, a.seq_len, int(p.t0));
+    const long long f_beg = seq_begin(a.cu, a.seq_len, nf), f_end = seq_begin(a.cu, a.seq_len, nf + 1);
+    {
+        f2 h[kP];
+#pragma unroll
+        for (int i = 0; i < kP; ++i) h[i] = 0ull;
+        const long long base = (long long)p.b * a.S;
+        if (live && f_beg < p.t0) {
+            const int sb = int((f_beg - p.row0) / a.L);
+            load_pairs<NP>(h, a.seg_h + (base + sb) * row + at, a.N);
+            for (int i = sb + 1; i < p.s; ++i) {
+                f2 e[kP];
+                load_pairs<NP>(e, a.seg_h + (base + i) * row + at, a.N);
+                const f2 sd = dup2(a.seg_d[(base + i) * a.D + d]);
+#pragma unroll
+                for (int k = 0; k < kP; ++k) h[k] = fma2(decay(A2[k], sd), h[k], e[k]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            ulonglong2 v;
+            v.x = h[2 * i];
+            v.y = h[2 * i + 1];
+            *reinterpret_cast<ulonglong2*>(&sm.hin[swz<NP>(lane, i)]) = v;
+        }
+        const int nl = seq_of(a.cu, a.nseq, a.seq_len, int(p.t1 - 1));
+        const long long l_end = seq_begin(a.cu, a.seq_len, nl + 1);
+        if (live && l_end > p.t1) {
+#pragma unroll
+            for (int k = 0; k < kP; ++k) h[k] = dup2(1.f);  // the decay from t1 to the segment looked at
+            for (int i = p.s + 1; i < a.S; ++i) {
+                f2 e[kP];
+                load_pairs<NP>(e, a.seg_g + (base + i) * row + at, a.N);
+                const f2 sd = dup2(a.seg_d[(base + i) * a.D + d]);
+#pragma unroll
+                for (int k = 0; k < kP; ++k) {
+                    g[k] = fma2(h[k], e[k], g[k]);
+                    h[k] = mul2(h[k], decay(A2[k], sd));
+                }
+                if (l_end <= p.row0 + (long long)(i + 1) * a.L) break;
+            }
+        }
+    }
+    if (!live)  // lanes without a channel take part in the sums over channels: their inputs are 0
+        for (int w = 0; w < 2; ++w) {
+            for (int k = 0; k < kMT; ++k)
+                sm.u[w][k][lane] = sm.dt[w][k][lane] = sm.z[w][k][lane] = sm.dy[w][k][lane] = from_f32<T>(0.f);
+            for (int j = 0; j < Smem::kChunks; ++j) {
+                sm.ckd[w][j][lane] = 0.f;
+                for (int i = 0; i < NP; ++i) sm.ck[w][j][lane * NP + i] = 0.f;
+            }
+        }
+    const long long chunk0 = si * (a.L / KC);
+    auto request = [&](long long tt, int w) {
+        const int m = int(p.t1 - tt < kMT ? p.t1 - tt : kMT);
+        stage_tile<T, kVec>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
+        stage_tile<T, kVec>(sm.dt[w], a.dt, tt, m, a.lddt, p.d0, valid, lane);
+        stage_tile<T, kVec>(sm.dy[w], a.dy, tt, m, a.lddy, p.d0, valid, lane);
+        if (a.z) stage_tile<T, kVec>(sm.z[w], a.z, tt, m, a.ldz, p.d0, valid, lane);
+        stage_bc<T, NP>(sm.b[w], a.Bm, tt, m, a.ldb, (long long)p.g * a.N, a.N, bc_vec, lane);
+        stage_bc<T, NP>(sm.c[w], a.Cm, tt, m, a.ldc, (long long)p.g * a.N, a.N, bc_vec, lane);
+        if (live)
+#pragma unroll
+            for (int j = 0; j < Smem::kChunks; ++j)
+                if (j * KC < m) {
+                    const long long ck = (chunk0 + (tt - p.t0) / KC + j) * a.D + d;
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) cp_async<16>(&sm.ck[w][j][swz<NP>(lane, i)], a.ckpt + ck * NP + 4 * i);
+                    cp_async<4>(&sm.ckd[w][j][lane], a.ckpt_d + ck);
+                }
+        cp_async_commit();
+    };
+    float aD = 0.f, ab = 0.f;  // dDskip, dbias of the channel
+    const int tiles = int((p.t1 - p.t0 + kMT - 1) / kMT);
+    request(p.t0 + (long long)(tiles - 1) * kMT, 0);
+    int buf = 0;
+    float* const part = a.part_bc + ((((long long)(blockIdx.x % a.bpg) * a.rows * a.row_len) * a.G + p.g) * 2) * a.N;
+    for (int ti = tiles - 1; ti >= 0; --ti, buf ^= 1) {
+        const long long tt = p.t0 + (long long)ti * kMT;
+        const int steps = int(p.t1 - tt < kMT ? p.t1 - tt : kMT);
+        int ef = -1, el = -1;
+        if (lane < kMT) {
+            // (a tile strictly inside the segment's first or last sequence needs no search)
+            edge_flags(a, tt + lane, lane < steps, ef, el);
+            sm.first[lane] = ef;
+            sm.last[lane] = el;
+        }
+        const bool edges = __any_sync(0xffffffffu, ef >= 0 || el >= 0);
+        cp_async_wait0();
+        __syncwarp();
+        widen_rows<T, NP>(sm.bc, 0, sm.b[buf], lane);
+        widen_rows<T, NP>(sm.bc, NP, sm.c[buf], lane);
+        if (steps < kMT) {  // tokens past the end: B = C = 0
+            __syncwarp();
+            for (int i = steps * 2 * NP + lane; i < kMT * 2 * NP; i += 32) (&sm.bc[0][0])[i] = 0.f;
+        }
+        __syncwarp();
+        if (ti > 0) request(tt - kMT, buf ^ 1);
+        auto walk = [&](auto has_edges) {
+            constexpr bool kEdges = decltype(has_edges)::value;
+#pragma unroll 1
+            for (int k0 = (steps - 1) / KC * KC; k0 >= 0; k0 -= KC) {
+                f2 h[kP], av[KC][kP], hp[KC][kP];
+                float Dv[KC], uv[KC], pv[KC], ys[KC];
+                // forward from the checkpoint
+                {
+                    const int j = k0 / KC;
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) {
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&sm.ck[buf][j][swz<NP>(lane, i)]);
+                        h[2 * i] = v.x;
+                        h[2 * i + 1] = v.y;
+                    }
+                    if (f_beg < p.t0 && tt + k0 < f_end) {  // it counts from zero: add the incoming state's part
+                        const f2 sd = dup2(sm.ckd[buf][j][lane]);
+#pragma unroll
+                        for (int i = 0; i < kV; ++i) {
+                            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&sm.hin[swz<NP>(lane, i)]);
+                            h[2 * i] = fma2(decay(A2[2 * i], sd), v.x, h[2 * i]);
+                            h[2 * i + 1] = fma2(decay(A2[2 * i + 1], sd), v.y, h[2 * i + 1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < KC; ++j) {
+                    const int k = k0 + j;
+                    const bool in = k < steps;  // tokens past the end: D = 0, p = 0
+                    if (kEdges && sm.first[k] >= 0) {
+#pragma unroll
+                        for (int i = 0; i < kP; ++i) h[i] = 0ull;
+                        if (a.h0 && live) load_pairs<NP>(h, a.h0 + sm.first[k] * row + at, a.N);
+                    }
+                    float D = to_f32<T>(sm.dt[buf][k][lane]) + bias;
+                    if (a.softplus) D = softplus_poly(D);
+                    Dv[j] = in ? D : 0.f;
+                    uv[j] = in ? to_f32<T>(sm.u[buf][k][lane]) : 0.f;
+                    pv[j] = in ? to_f32<T>(sm.dy[buf][k][lane]) : 0.f;
+                    if (a.z && in) pv[j] *= siluf(to_f32<T>(sm.z[buf][k][lane]));
+                    const f2 D2 = dup2(Dv[j]), w2 = dup2(Dv[j] * uv[j]);
+                    f2 s = 0ull;
+#pragma unroll
+                    for (int i = 0; i < kP; i += 2) {
+                        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&sm.bc[k][2 * i]);
+                        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&sm.bc[k][NP + 2 * i]);
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            av[j][i + v] = decay(A2[i + v], D2);
+                            hp[j][i + v] = h[i + v];
+                            h[i + v] = fma2(av[j][i + v], h[i + v], mul2(w2, v ? b.y : b.x));
+                            s = fma2(h[i + v], v ? c.y : c.x, s);
+                        }
+                    }
+                    ys[j] = lo2(s) + hi2(s);
+                }
+                // and back
+#pragma unroll
+                for (int j = KC - 1; j >= 0; --j) {
+                    const int k = k0 + j;
+                    if (k >= steps) continue;
+                    if (kEdges && sm.last[k] >= 0) {
+#pragma unroll
+                        for (int i = 0; i < kP; ++i) g[i] = 0ull;
+                        if (a.dhT && live) load_pairs<NP>(g, a.dhT + sm.last[k] * row + at, a.N);
+                    }
+                    const f2 D2 = dup2(Dv[j]), w2 = dup2(Dv[j] * uv[j]), p2 = dup2(pv[j]);
+                    f2 sgb = 0ull, sea = 0ull;
+#pragma unroll
+                    for (int i = 0; i < kP; i += 2) {
+                        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&sm.bc[k][2 * i]);
+                        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&sm.bc[k][NP + 2 * i]);
+                        f2 db[2], dc[2];
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const f2 bv = v ? b.y : b.x;
+                            g[i + v] = fma2(v ? c.y : c.x, p2, g[i + v]);
+                            const f2 ah = mul2(av[j][i + v], hp[j][i + v]);
+                            const f2 e = mul2(g[i + v], ah);
+                            db[v] = mul2(g[i + v], w2);
+                            dc[v] = mul2(p2, fma2(w2, bv, ah));
+                            sgb = fma2(g[i + v], bv, sgb);
+                            sea = fma2(e, A2[i + v], sea);
+                            dA[i + v] = fma2(e, D2, dA[i + v]);
+                            g[i + v] = mul2(g[i + v], av[j][i + v]);
+                        }
+                        channel_sum_write<NP>(sm.sum, j & 1, lane, 2 * i, db[0], db[1]);
+                        channel_sum_write<NP>(sm.sum, j & 1, lane, NP + 2 * i, dc[0], dc[1]);
+                    }
+                    if (kEdges && sm.first[k] >= 0 && a.dh0 && live) store_pairs<NP>(g, a.dh0 + sm.first[k] * row + at, a.N);
+                    __syncwarp();  // (the next token writes the other buffer)
+                    channel_sum_read<NP>(sm.sum, j & 1, lane, part + (tt + k) * a.G * 2 * a.N, a.N);
+                    const float gb = lo2(sgb) + hi2(sgb), ea = (lo2(sea) + hi2(sea)) * 0.69314718055994531f;
+                    float ddt = gb * uv[j] + ea;
+                    if (a.softplus) ddt *= sigmoidf(to_f32<T>(sm.dt[buf][k][lane]) + bias);
+                    aD += pv[j] * uv[j];
+                    ab += ddt;
+                    if (live) {
+                        static_cast<T*>(a.du)[(tt + k) * a.lddu + d] = from_f32<T>(gb * Dv[j] + skip * pv[j]);
+                        static_cast<T*>(a.ddt)[(tt + k) * a.ldddt + d] = from_f32<T>(ddt);
+                        if (a.z)
+                            static_cast<T*>(a.dz)[(tt + k) * a.lddz + d] = from_f32<T>(
+                                to_f32<T>(sm.dy[buf][k][lane]) * (ys[j] + skip * uv[j]) * dsilu(to_f32<T>(sm.z[buf][k][lane])));
+                    }
+                }
+            }
+        };
+        if (edges) walk(std::true_type{});
+        else walk(std::false_type{});
+        __syncwarp();
+    }
+    if (live) {
+        store_pairs<NP>(dA, a.part_a + si * row + at, a.N);
+        a.part_d[si * 2 * a.D + d] = aD;
+        a.part_d[(si * 2 + 1) * a.D + d] = ab;
     }
 }
 
@@ -183,6 +553,8 @@ __device__ __forceinline__ void channel_sum(float (&v)[2 * R], int lane) {
     }
 }
 
+// The second pass for 17 to 32 states, which do not fit one lane's registers: a quad of
+// lanes holds a channel, R = 8 states each; a block holds 32 channels.
 template <int R>
 struct BwdSmem {
     float4 s[kTT][kCh];  // D, D u, p
@@ -194,8 +566,8 @@ struct BwdSmem {
 };
 
 template <typename T, int R, bool kVec>
-__global__ void __launch_bounds__(128) bwd_kernel(const SArgs a, bool bc_vec) {
-    constexpr int KC = 32 / R;
+__global__ void __launch_bounds__(128) bwd_quad_kernel(const SArgs a, bool bc_vec) {
+    constexpr int KC = ckpt_tokens(4 * R);
     extern __shared__ __align__(16) uint8_t smem_raw[];
     BwdSmem<R>& sm = *reinterpret_cast<BwdSmem<R>*>(smem_raw);
     const int tid = threadIdx.x, q = tid & 3, c = tid >> 2, lane = tid & 31, warp = tid >> 5;
@@ -206,7 +578,7 @@ __global__ void __launch_bounds__(128) bwd_kernel(const SArgs a, bool bc_vec) {
     float A2[R], g[R], hin[R], dA[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        A2[r] = live && n0 + r < a.N ? a.A[(size_t)d * a.N + n0 + r] * kLog2e : 0.f;
+        A2[r] = live && n0 + r < a.N ? a.A[(size_t)d * a.N + n0 + r] * kL2e : 0.f;
         g[r] = hin[r] = dA[r] = 0.f;
     }
     if (tid < kCh) {
@@ -306,6 +678,8 @@ __global__ void __launch_bounds__(128) bwd_kernel(const SArgs a, bool bc_vec) {
         const bool edges = __syncthreads_or(ef >= 0 || el >= 0);
         if (ti > 0) request(tt - kTT);
         const int steps = int(p.t1 - tt < kTT ? p.t1 - tt : kTT);
+        auto walk = [&](auto has_edges) {  // two bodies, as in the forward pass
+        constexpr bool kEdges = decltype(has_edges)::value;
 #pragma unroll 1
         for (int k0 = (steps - 1) / KC * KC; k0 >= 0; k0 -= KC) {
             const long long tc = tt + k0, ck = chunk0 + (tc - p.t0) / KC;
@@ -313,7 +687,7 @@ __global__ void __launch_bounds__(128) bwd_kernel(const SArgs a, bool bc_vec) {
 #pragma unroll
             for (int r = 0; r < R; ++r) h[r] = 0.f;
             if (live) {
-                load_h<R>(h, a.ckpt + (ck * a.D + d) * a.N, n0, a.N);
+                load_h<R>(h, a.ckpt + (ck * a.D + d) * (4 * R), n0, a.N);
                 if (f_beg < p.t0 && tc < f_end) {  // the checkpoint counts from zero: add the incoming state's part
                     const float sd = a.ckpt_d[ck * a.D + d];
 #pragma unroll
@@ -326,7 +700,7 @@ __global__ void __launch_bounds__(128) bwd_kernel(const SArgs a, bool bc_vec) {
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
                     const int j = j4 + jj, k = k0 + j;
-                    if (edges && sm.first[k] >= 0) {
+                    if (kEdges && sm.first[k] >= 0) {
 #pragma unroll
                         for (int r = 0; r < R; ++r) h[r] = 0.f;
                         if (a.h0 && live) load_h<R>(h, a.h0 + ((size_t)sm.first[k] * a.D + d) * a.N, n0, a.N);
@@ -341,7 +715,7 @@ __global__ void __launch_bounds__(128) bwd_kernel(const SArgs a, bool bc_vec) {
                         acc[jj] += h[r] * sm.c[k][n0 + r];
                     }
                 }
-                sm.hc[k0 + j4 + q][c] = quad_transpose_sum(acc, q);
+                sm.hc[k0 + j4 + q][c] = lane_transpose_sum<4>(acc, q);
             }
 #pragma unroll
             for (int j4 = KC - 4; j4 >= 0; j4 -= 4) {
@@ -350,7 +724,7 @@ __global__ void __launch_bounds__(128) bwd_kernel(const SArgs a, bool bc_vec) {
                 for (int jj = 3; jj >= 0; --jj) {
                     const int j = j4 + jj, k = k0 + j;
                     const float4 s = sm.s[k][c];
-                    if (edges && sm.last[k] >= 0) {
+                    if (kEdges && sm.last[k] >= 0) {
 #pragma unroll
                         for (int r = 0; r < R; ++r) g[r] = 0.f;
                         if (a.dhT && live) load_h<R>(g, a.dhT + ((size_t)sm.last[k] * a.D + d) * a.N, n0, a.N);
@@ -370,7 +744,7 @@ __global__ void __launch_bounds__(128) bwd_kernel(const SArgs a, bool bc_vec) {
                         dA[r] += e * s.x;
                         g[r] *= av[j][r];
                     }
-                    if (edges && sm.first[k] >= 0 && a.dh0 && live)
+                    if (kEdges && sm.first[k] >= 0 && a.dh0 && live)
                         store_h<R>(g, a.dh0 + ((size_t)sm.first[k] * a.D + d) * a.N, n0, a.N);
                     channel_sum<R>(v, lane);
                     // value number b4 R + b3 R/2 + ... of the list [dB | dC] of this lane's states
@@ -384,10 +758,13 @@ __global__ void __launch_bounds__(128) bwd_kernel(const SArgs a, bool bc_vec) {
                         o[((lane >> 1) & 4) + ((lane >> 1) & 2) + 1] = v[1];
                     }
                 }
-                sm.gb[k0 + j4 + q][c] = quad_transpose_sum(agb, q);
-                sm.ea[k0 + j4 + q][c] = quad_transpose_sum(aea, q);
+                sm.gb[k0 + j4 + q][c] = lane_transpose_sum<4>(agb, q);
+                sm.ea[k0 + j4 + q][c] = lane_transpose_sum<4>(aea, q);
             }
         }
+        };
+        if (edges) walk(std::true_type{});
+        else walk(std::false_type{});
         __syncthreads();
         if (here) {
             float odu[8], odt[8], odz[8];
@@ -456,14 +833,20 @@ __global__ void __launch_bounds__(256) bwd_bc_sum_kernel(const float* __restrict
 
 // Segments of the backward pass: the map pass runs in any case (checkpoints), so they
 // may be shorter than the forward pass's.
-static Cut bwd_cut(int B, int T, int D, int G, bool packed) {
+static Cut bwd_cut(int B, int T, int D, int G, int N, bool packed) {
     Cut c{};
     c.rows = packed ? 1 : B;
     c.row_len = T;
     c.bpg = int(cdiv(D / G, kCh));
     const long long blocks = (long long)c.rows * G * c.bpg;
-    long long S = cdiv((long long)device_sm_count() * 3, blocks);
-    const long long most = T / 128 < 32 ? T / 128 : 32;
+    // Up to 16 states the second pass holds 8 warps an SM (its registers): one full wave of
+    // warps (8192 tokens of 4096 channels in all: 8 segments 380 us, 12 485 us, 16 394 us).
+    // Above, 4 blocks of 4 warps an SM.
+    long long S = N <= 16 ? 8ll * device_sm_count() / blocks : cdiv(4ll * device_sm_count(), blocks);
+#ifdef KDA_SCAN_TUNE
+    if (getenv("KDA_SB")) S = atoi(getenv("KDA_SB"));
+#endif
+    const long long most = T / 64 < 64 ? T / 64 : 64;
     if (S > most) S = most;
     if (S < 1) S = 1;
     c.L = int(cdiv(cdiv(T, S), kTT) * kTT);
@@ -477,9 +860,9 @@ struct BwdPlan {
 };
 static BwdPlan bwd_plan(int B, int T, int D, int G, int N, bool packed) {
     BwdPlan p{};
-    p.c = bwd_cut(B, T, D, G, packed);
-    const size_t segs = size_t(p.c.rows) * p.c.S, KC = 32 / states_per_lane(N);
-    const size_t chunks = segs * (p.c.L / KC), toks = size_t(p.c.rows) * T;
+    p.c = bwd_cut(B, T, D, G, N, packed);
+    const int NP = padded_states(N);
+    const size_t segs = size_t(p.c.rows) * p.c.S, chunks = segs * (p.c.L / ckpt_tokens(NP)), toks = size_t(p.c.rows) * T;
     size_t off = 0;
     auto take = [&](size_t floats) {
         const size_t at = off;
@@ -489,7 +872,7 @@ static BwdPlan bwd_plan(int B, int T, int D, int G, int N, bool packed) {
     p.off_segh = take(segs * D * N);
     p.off_segd = take(segs * D);
     p.off_segg = take(segs * D * N);
-    p.off_ckpt = take(chunks * D * N);
+    p.off_ckpt = take(chunks * D * NP);
     p.off_ckptd = take(chunks * D);
     p.off_bc = take(size_t(p.c.bpg) * toks * G * 2 * N);
     p.off_a = take(segs * D * N);
@@ -504,33 +887,38 @@ struct BwdOut {
     float *dA, *dskip, *dbias;
 };
 
-template <typename T, int R, bool kVec>
-int bwd_vec(const SArgs& a, const BwdOut& o, bool bc, cudaStream_t st) {
+template <typename T, int NP, bool kVec>
+int bwd_run(const SArgs& a, const BwdOut& o, bool bc, cudaStream_t st) {
     const dim3 grid(a.G * a.bpg, a.rows * a.S);
-    bwd_map_kernel<T, R, kVec><<<grid, 128, 0, st>>>(a, bc);
-    auto kern = bwd_kernel<T, R, kVec>;
-    if (!set_smem_attr(kern, sizeof(BwdSmem<R>))) return KDA_ERR_CUDA;
-    kern<<<grid, 128, sizeof(BwdSmem<R>), st>>>(a, bc);
+    bwd_map_kernel<T, NP, kVec><<<grid, 32, 0, st>>>(a, bc);
+    if constexpr (NP <= 16) {
+        auto kern = bwd_kernel<T, NP, kVec>;
+        if (!set_smem_attr(kern, sizeof(MainSmem<T, NP>))) return KDA_ERR_CUDA;
+        kern<<<grid, 32, sizeof(MainSmem<T, NP>), st>>>(a, bc);
+    } else {
+        auto kern = bwd_quad_kernel<T, NP / 4, kVec>;
+        if (!set_smem_attr(kern, sizeof(BwdSmem<NP / 4>))) return KDA_ERR_CUDA;
+        kern<<<grid, 128, sizeof(BwdSmem<NP / 4>), st>>>(a, states_ok(a, sizeof(T), NP / 4));
+    }
     const long long total = (long long)a.rows * a.row_len * a.G * 2 * a.N;
     bwd_bc_sum_kernel<T><<<unsigned(cdiv(total, 256)), 256, 0, st>>>(a.part_bc, a.bpg, total, a.G, a.N,
                                                                      static_cast<T*>(o.dB), o.lddb,
                                                                      static_cast<T*>(o.dC), o.lddc);
     const int segs = a.rows * a.S;
     const long long dn = (long long)a.D * a.N;
-    sum_parts_kernel<float><<<unsigned(cdiv(dn, 32)), 256, 0, st>>>(a.part_a, segs, dn, o.dA, dn);
-    if (o.dskip) sum_parts_kernel<float><<<unsigned(cdiv(a.D, 32)), 256, 0, st>>>(a.part_d, segs, 2ll * a.D, o.dskip, a.D);
-    if (o.dbias)
-        sum_parts_kernel<float><<<unsigned(cdiv(a.D, 32)), 256, 0, st>>>(a.part_d + a.D, segs, 2ll * a.D, o.dbias, a.D);
+    sum_parts<float>(a.part_a, segs, dn, o.dA, nullptr, dn, st);
+    sum_parts<float>(a.part_d, segs, 2ll * a.D, o.dskip, o.dbias, a.D, st);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-template <typename T, int R>
+template <typename T>
 int bwd(const SArgs& a, const BwdOut& o, cudaStream_t st) {
     const void* ptrs[] = {a.u, a.dt, a.z, a.dy, a.du, a.ddt, a.dz};
     const long long lds[] = {a.ldu, a.lddt, a.ldz, a.lddy, a.lddu, a.ldddt, a.lddz};
-    const bool bc = states_ok(a, sizeof(T), R);
-    if (vec8_ok(a, sizeof(T), ptrs, lds, 7)) return bwd_vec<T, R, true>(a, o, bc, st);
-    return bwd_vec<T, R, false>(a, o, bc, st);
+    const bool vec = vec8_ok(a, sizeof(T), ptrs, lds, 7), bc = bc_whole(a, sizeof(T));
+    if (a.N <= 8) return vec ? bwd_run<T, 8, true>(a, o, bc, st) : bwd_run<T, 8, false>(a, o, bc, st);
+    if (a.N <= 16) return vec ? bwd_run<T, 16, true>(a, o, bc, st) : bwd_run<T, 16, false>(a, o, bc, st);
+    return vec ? bwd_run<T, 32, true>(a, o, bc, st) : bwd_run<T, 32, false>(a, o, bc, st);
 }
 
 }  // namespace scan
@@ -552,7 +940,7 @@ int launch_selective_scan_bwd(scan::SArgs a, const scan::BwdOut& o, int B, int t
     a.part_bc = reinterpret_cast<float*>(b + p.off_bc);
     a.part_a = reinterpret_cast<float*>(b + p.off_a);
     a.part_d = reinterpret_cast<float*>(b + p.off_d);
-    KDA_SCAN_DISPATCH(a.N, (scan::bwd<T, R>(a, o, st)))
+    return dtype == KDA_BF16 ? scan::bwd<__nv_bfloat16>(a, o, st) : scan::bwd<float>(a, o, st);
 }
 
 }  // namespace kda
