@@ -30,7 +30,9 @@ enum Act { kNone = KDA_ACT_NONE, kRelu = KDA_ACT_RELU, kGelu = KDA_ACT_GELU, kSi
 template <int kBN, bool kPre>
 struct LPlan {
     static constexpr uint32_t kB = kBN * BK * 2, kStage = kABytes + kB;
-    static constexpr uint32_t kStagingBytes = kPre ? 8192 : 4096;  // per epilogue warp: a tile of y, one of s
+    // per epilogue warp: one tile, for s and then for y (a tile for each would cost the
+    // fourth stage: 516 us against 400 at 16384 x 8192 x 2048 with the pre-activation)
+    static constexpr uint32_t kStagingBytes = 4096;
     // as many stages as fit beside the staging tiles and the barriers, at most 8
     static constexpr int kFit = int((232448 - 1280 - kEpiWarps * kStagingBytes) / kStage);
     static constexpr int kStages = kFit < 8 ? kFit : 8;
@@ -59,12 +61,47 @@ __device__ __forceinline__ void store_ragged(__nv_bfloat16* row, const float* v,
         if (j >= first && j < cols) row[j] = __float2bfloat16_rn(v[j]);
 }
 
-__device__ __forceinline__ float gelu(float x) { return 0.5f * x * (1.f + erff(x * 0.70710678118654752f)); }
+// 1 - Phi(|x|) = erfc(|x| / sqrt 2) / 2 and e^{-x^2/2}.  erfc(z) = e^{-z^2} t S(t) with t =
+// 1 / (1 + z / 2); S is a polynomial fitted to a relative 1.4e-6 over z in [0, 10], beyond
+// which the product is below the smallest bf16.  Relative accuracy in the tail matters
+// (x Phi(x) for negative x), so erf's absolute error bounds would not do; and the
+// two-branch erff made the epilogue, not the tensor cores, the bound of a wide GELU
+// projection (16384 x 8192 x 2048: 552 us, now 399).
+__device__ __forceinline__ float phi_tail(float x, float& gauss) {
+    const float z = fabsf(x) * 0.70710678118654752f;
+    const float t = mix::rcp(fmaf(0.5f, z, 1.f));
+    gauss = mix::ex2(z * z * -1.4426950408889634f);
+    float s = fmaf(0.08820453f, t, -0.35673877f);
+    s = fmaf(s, t, 0.38922512f);
+    s = fmaf(s, t, 0.03789042f);
+    s = fmaf(s, t, 0.28150379f);
+    s = fmaf(s, t, 0.27758215f);
+    s = fmaf(s, t, 0.28233141f);
+    return 0.5f * gauss * t * s;
+}
+__device__ __forceinline__ float gelu(float x) {
+    float g;
+    const float q = phi_tail(x, g);
+    return x * (x > 0.f ? 1.f - q : q);
+}
 // softplus with the fast log: the result is rounded to bf16.  Below -8 the sum 1 + e^x
 // keeps too few bits of e^x, and log(1 + e^x) is e^x to within e^x / 2 < 2^-12 of it.
 __device__ __forceinline__ float softplus_bf16(float x) {
     const float e = __expf(-fabsf(x));
     return fmaxf(x, 0.f) + (e < 3.3e-4f ? e : __logf(1.f + e));
+}
+
+// Outputs and the residual pass once: stored and loaded as the first lines to leave L2,
+// which W and the rows of x in flight need.
+__device__ __forceinline__ uint64_t policy_evict_first() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_store_2d_once(const CUtensorMap* map, const void* src, int c0, int c1, uint64_t policy) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%2, %3}], [%1], %4;" ::"l"(map),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "l"(policy)
+                 : "memory");
 }
 
 template <int kN>
@@ -80,7 +117,7 @@ __device__ __forceinline__ void apply_act(float* v, int act) {
             break;
         case kSilu:
 #pragma unroll
-            for (int j = 0; j < kN; ++j) v[j] = __fdividef(v[j], 1.f + __expf(-v[j]));
+            for (int j = 0; j < kN; ++j) v[j] = mix::siluf(v[j]);
             break;
         case kSoftplus:
 #pragma unroll
@@ -232,6 +269,7 @@ __global__ void __launch_bounds__(gemm::kThreads, 1)
         const int quad = warp & 3;   // TMEM lane quadrant this warp may read
         const int half = ew >> 2;    // column half of the tile (a 64-wide tile has one)
         constexpr int kChunks = kBN >= 128 ? kBN / 128 : 1;
+        const uint64_t policy = policy_evict_first();
         const uint32_t stg = sbase + P::OFF_STAGING + uint32_t(ew) * P::kStagingBytes;
         uint8_t* stg_p = sm + P::OFF_STAGING + ew * P::kStagingBytes;
         int i = 0;
@@ -249,7 +287,7 @@ __global__ void __launch_bounds__(gemm::kThreads, 1)
                     const __nv_bfloat16* r = p.res + (size_t)row * p.ldr + n0 + c0;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (c0 + 8 * j + 8 <= cols) res[j] = __ldg(reinterpret_cast<const uint4*>(r) + j);
+                        if (c0 + 8 * j + 8 <= cols) res[j] = __ldcs(reinterpret_cast<const uint4*>(r) + j);
                 }
             };
             const int h0 = kBN >= 128 ? half * (kBN / 2) : 0;
@@ -295,7 +333,13 @@ __global__ void __launch_bounds__(gemm::kThreads, 1)
                     if (ragged) store_ragged<64>(p.pre + (size_t)row * p.ldp + n0 + c0, v, whole, cols - c0);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) w32[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
-                    stage_row(stg + 4096, lane, w32);
+                    stage_row(stg, lane, w32);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && whole > 0) {
+                        tma_store_2d_once(&map_p, stg_p, n0 + c0, m0 + quad * 32, policy);
+                        gemm::bulk_commit();
+                    }
                 }
                 apply_act<64>(v, p.act);
                 if (p.res && row < p.M) {
@@ -324,12 +368,15 @@ __global__ void __launch_bounds__(gemm::kThreads, 1)
                 if (ragged) store_ragged<64>(p.c + (size_t)row * p.ldc + n0 + c0, v, whole, cols - c0);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) w32[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
+                if constexpr (kPre) {
+                    if (lane == 0) gemm::bulk_wait_read0();  // the store of s has read the tile
+                    __syncwarp();
+                }
                 stage_row(stg, lane, w32);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0 && whole > 0) {
-                    tma_store_2d(&map_c, stg_p, n0 + c0, m0 + quad * 32);
-                    if (kPre) tma_store_2d(&map_p, stg_p + 4096, n0 + c0, m0 + quad * 32);
+                    tma_store_2d_once(&map_c, stg_p, n0 + c0, m0 + quad * 32, policy);
                     gemm::bulk_commit();
                 }
             }
@@ -383,17 +430,134 @@ static int launch_tile(const void* A, int lda, const void* B, int ldb, void* C, 
     return KDA_OK;
 }
 
+// Tile width by the SMs it fills: the cost of a width is its waves of tiles times the
+// columns of a tile, plus what a tile costs whatever its width (the A operand's share
+// of the loads).
+static int tile_width(int M, int N) {
+    const long long sms = device_sm_count(), tm = (M + BM - 1) / BM;
+    int best = 256;
+    long long least = 0;
+    for (int bn = 256; bn >= 64; bn /= 2) {
+        const long long waves = mix::cdiv(tm * ((N + bn - 1) / bn), sms), cost = waves * (bn + 64);
+        if (bn == 256 || cost < least) {
+            best = bn;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 template <bool kAMN, bool kBMN, bool kPre>
 static int launch(const void* A, int lda, const void* B, int ldb, void* C, int ldc, void* pre, int ldp, const LArgs& a,
                   cudaStream_t st, const char** why) {
-    return launch_tile<256, kAMN, kBMN, kPre>(A, lda, B, ldb, C, ldc, pre, ldp, a, st, why);
+    switch (tile_width(a.M, a.N)) {
+        case 256: return launch_tile<256, kAMN, kBMN, kPre>(A, lda, B, ldb, C, ldc, pre, ldp, a, st, why);
+        case 128: return launch_tile<128, kAMN, kBMN, kPre>(A, lda, B, ldb, C, ldc, pre, ldp, a, st, why);
+        default: return launch_tile<64, kAMN, kBMN, kPre>(A, lda, B, ldb, C, ldc, pre, ldp, a, st, why);
+    }
+}
+
+__device__ __forceinline__ float act1(float x, int act) {
+    float v[1] = {x};
+    apply_act<1>(v, act);
+    return v[0];
+}
+
+// Few rows of x (decode): bound by reading W once.  A block has 16 rows of W (outputs);
+// its 16 warps take slices of K and add their sums in shared memory, in order.  Warp
+// MMAs (m16n8k16) with W as the 16-row operand and up to 8 kMT rows of x as columns: the
+// sum over k has no order, so a thread's fragments are 8 neighbouring values of its
+// rows, and W goes from memory to registers in 16-byte loads, without shared memory.
+// 16 x 2048 x 4096: 5.4 us; 128-row tiles of the kernel above leave most SMs idle and
+// 112 of 128 rows empty (32 us).
+constexpr int kSkinnyWarps = 16;
+template <int kMT>
+__global__ void __launch_bounds__(32 * kSkinnyWarps)
+    skinny_kernel(const __nv_bfloat16* __restrict__ x, int ldx, const __nv_bfloat16* __restrict__ W, int ldw,
+                  const LArgs p) {
+    __shared__ float red[kSkinnyWarps][16][8 * kMT + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int n0 = blockIdx.x * 16;
+    // K in steps of 32 (8 values a thread), dealt to the warps in runs
+    const int steps = (p.K + 31) / 32, per = (steps + kSkinnyWarps - 1) / kSkinnyWarps;
+    const int s0 = warp * per, s1 = min(steps, s0 + per);
+    float acc[kMT][4];
+#pragma unroll
+    for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+    const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N;
+    const __nv_bfloat16 *w0 = W + (size_t)(n0 + g) * ldw, *w1 = W + (size_t)(n0 + g + 8) * ldw;
+    constexpr int kU = kMT <= 2 ? 8 : 4;  // steps in flight
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int sb = s0; sb < s1; sb += kU) {
+        uint4 a0[kU], a1[kU];
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+            const int k = (sb + i) * 32 + t * 8;
+            const bool in = sb + i < s1 && k < p.K;
+            a0[i] = in && in0 ? __ldcs(reinterpret_cast<const uint4*>(w0 + k)) : zero;
+            a1[i] = in && in1 ? __ldcs(reinterpret_cast<const uint4*>(w1 + k)) : zero;
+        }
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+            const int k = (sb + i) * 32 + t * 8;
+            const bool in = sb + i < s1 && k < p.K;
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) {
+                const int row = m * 8 + g;
+                const uint4 b = in && row < p.M ? __ldg(reinterpret_cast<const uint4*>(x + (size_t)row * ldx + k)) : zero;
+                asm volatile(
+                    "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                    : "+f"(acc[m][0]), "+f"(acc[m][1]), "+f"(acc[m][2]), "+f"(acc[m][3])
+                    : "r"(a0[i].x), "r"(a1[i].x), "r"(a0[i].y), "r"(a1[i].y), "r"(b.x), "r"(b.y));
+                asm volatile(
+                    "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                    : "+f"(acc[m][0]), "+f"(acc[m][1]), "+f"(acc[m][2]), "+f"(acc[m][3])
+                    : "r"(a0[i].z), "r"(a1[i].z), "r"(a0[i].w), "r"(a1[i].w), "r"(b.z), "r"(b.w));
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {  // sums: rows g, g + 8 of W; columns (rows of x) 2t, 2t + 1
+        red[warp][g][m * 8 + 2 * t] = acc[m][0];
+        red[warp][g][m * 8 + 2 * t + 1] = acc[m][1];
+        red[warp][g + 8][m * 8 + 2 * t] = acc[m][2];
+        red[warp][g + 8][m * 8 + 2 * t + 1] = acc[m][3];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * 8 * kMT; i += 32 * kSkinnyWarps) {
+        const int n = n0 + (i & 15), row = i >> 4;
+        if (n >= p.N || row >= p.M) continue;
+        float v = p.bias ? p.bias[n] : 0.f;
+#pragma unroll
+        for (int w = 0; w < kSkinnyWarps; ++w) v += red[w][i & 15][row];
+        if (p.pre) p.pre[(size_t)row * p.ldp + n] = __float2bfloat16_rn(v);
+        v = act1(v, p.act);
+        if (p.res) v += __bfloat162float(p.res[(size_t)row * p.ldr + n]);
+        p.c[(size_t)row * p.ldc + n] = __float2bfloat16_rn(v);
+    }
+}
+
+template <int kMT>
+static int launch_skinny(const void* x, int ldx, const void* W, int ldw, const LArgs& a, cudaStream_t st,
+                         const char** why) {
+    skinny_kernel<kMT><<<unsigned(mix::cdiv(a.N, 16)), 32 * kSkinnyWarps, 0, st>>>(
+        static_cast<const __nv_bfloat16*>(x), ldx, static_cast<const __nv_bfloat16*>(W), ldw, a);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) return KDA_OK;
+    *why = cudaGetErrorString(e);
+    return KDA_ERR_CUDA;
 }
 
 __device__ __forceinline__ float dact(float x, int act) {
     switch (act) {
         case kRelu: return x > 0.f ? 1.f : 0.f;
-        case kGelu:
-            return 0.5f * (1.f + erff(x * 0.70710678118654752f)) + x * 0.39894228040143268f * __expf(-0.5f * x * x);
+        case kGelu: {
+            float g;
+            const float q = phi_tail(x, g);
+            return (x > 0.f ? 1.f - q : q) + x * 0.39894228040143268f * g;
+        }
         case kSilu: {
             const float g = mix::sigmoidf(x);
             return g * (1.f + x * (1.f - g));
@@ -477,6 +641,15 @@ int launch_linear_act(const void* x, int ldx, const void* W, int ldw, const floa
     a.ldr = ldr;
     a.res_vec = res && mix::al16(res) && ldr % 8 == 0;
     a.act = act;
+    if (M <= 32) {
+        a.c = static_cast<__nv_bfloat16*>(y);
+        a.ldc = ldy;
+        a.pre = static_cast<__nv_bfloat16*>(pre);
+        a.ldp = ldp;
+        if (M <= 8) return lin::launch_skinny<1>(x, ldx, W, ldw, a, st, why);
+        if (M <= 16) return lin::launch_skinny<2>(x, ldx, W, ldw, a, st, why);
+        return lin::launch_skinny<4>(x, ldx, W, ldw, a, st, why);
+    }
     if (pre) return lin::launch<false, false, true>(x, ldx, W, ldw, y, ldy, pre, ldp, a, st, why);
     return lin::launch<false, false, false>(x, ldx, W, ldw, y, ldy, nullptr, 0, a, st, why);
 }
