@@ -488,33 +488,32 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps)
         for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
     const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N;
     const __nv_bfloat16 *w0 = W + (size_t)(n0 + g) * ldw, *w1 = W + (size_t)(n0 + g + 8) * ldw;
-    constexpr int kU = kMT <= 2 ? 8 : 4;  // steps in flight
+    constexpr int kU = kMT == 1 ? 8 : (kMT == 2 ? 6 : 4);  // steps in flight, of W and of x: what the registers hold
     const uint4 zero = make_uint4(0, 0, 0, 0);
     for (int sb = s0; sb < s1; sb += kU) {
-        uint4 a0[kU], a1[kU];
+        uint4 a0[kU], a1[kU], b[kU][kMT];
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
             const int k = (sb + i) * 32 + t * 8;
             const bool in = sb + i < s1 && k < p.K;
             a0[i] = in && in0 ? __ldcs(reinterpret_cast<const uint4*>(w0 + k)) : zero;
             a1[i] = in && in1 ? __ldcs(reinterpret_cast<const uint4*>(w1 + k)) : zero;
+#pragma unroll
+            for (int m = 0; m < kMT; ++m)
+                b[i][m] = in && m * 8 + g < p.M ? __ldg(reinterpret_cast<const uint4*>(x + (size_t)(m * 8 + g) * ldx + k)) : zero;
         }
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
-            const int k = (sb + i) * 32 + t * 8;
-            const bool in = sb + i < s1 && k < p.K;
 #pragma unroll
             for (int m = 0; m < kMT; ++m) {
-                const int row = m * 8 + g;
-                const uint4 b = in && row < p.M ? __ldg(reinterpret_cast<const uint4*>(x + (size_t)row * ldx + k)) : zero;
                 asm volatile(
                     "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                     : "+f"(acc[m][0]), "+f"(acc[m][1]), "+f"(acc[m][2]), "+f"(acc[m][3])
-                    : "r"(a0[i].x), "r"(a1[i].x), "r"(a0[i].y), "r"(a1[i].y), "r"(b.x), "r"(b.y));
+                    : "r"(a0[i].x), "r"(a1[i].x), "r"(a0[i].y), "r"(a1[i].y), "r"(b[i][m].x), "r"(b[i][m].y));
                 asm volatile(
                     "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                     : "+f"(acc[m][0]), "+f"(acc[m][1]), "+f"(acc[m][2]), "+f"(acc[m][3])
-                    : "r"(a0[i].z), "r"(a1[i].z), "r"(a0[i].w), "r"(a1[i].w), "r"(b.z), "r"(b.w));
+                    : "r"(a0[i].z), "r"(a1[i].z), "r"(a0[i].w), "r"(a1[i].w), "r"(b[i][m].z), "r"(b[i][m].w));
             }
         }
     }

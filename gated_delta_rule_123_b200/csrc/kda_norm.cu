@@ -32,67 +32,202 @@ __device__ __forceinline__ float row_sum(float v, float* sred) {
     return v;
 }
 
+// The values of a vector, two to a register pair.
+template <typename T>
+__device__ __forceinline__ void pairs(const Raw<T, true>& r, f2 (&v)[Pack<T, true>::kN / 2]) {
+    float f[Pack<T, true>::kN];
+    r.get(f);
+#pragma unroll
+    for (int u = 0; u < Pack<T, true>::kN / 2; ++u) v[u] = pk(f[2 * u], f[2 * u + 1]);
+}
+
 // kTpr threads hold one row, kVpt vectors each; a block of max(kTpr, 128) threads.
 template <typename T, int kTpr, int kVpt>
-__global__ void __launch_bounds__(kTpr > 128 ? kTpr : 128)
+__global__ void __launch_bounds__(kTpr == 32 ? 128 : kTpr)
     fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ b,
                T* __restrict__ y, long long ldy, float* __restrict__ mean, float* __restrict__ rstd, int M, int N,
                float eps) {
-    constexpr int kE = Pack<T, true>::kN, kRows = kTpr > 128 ? 1 : 128 / kTpr;
+    constexpr int kE = Pack<T, true>::kN, kRows = kTpr == 32 ? 4 : 1;
     __shared__ float sred[2][kTpr > 32 ? kTpr / 32 : 1];
-    const int t = threadIdx.x % kTpr;
-    const long long row = (long long)blockIdx.x * kRows + threadIdx.x / kTpr;
-    if (kTpr == 32 && row >= M) return;  // whole warps; with one row per block the grid is exact
-    const T* xr = x + row * ldx;
-    Raw<T, true> raw[kVpt];
-    const int nvec = N / kE;
+    const int t = threadIdx.x % kTpr, nvec = N / kE;
+    long long row = (long long)blockIdx.x * kRows + threadIdx.x / kTpr;
+    const long long step = (long long)gridDim.x * kRows;
+    if (row >= M) return;  // whole warps; with one row per block the grid is exact
+    for (; row < M; row += step) {
+        Raw<T, true> raw[kVpt];
 #pragma unroll
-    for (int i = 0; i < kVpt; ++i) {
-        const int j = t + i * kTpr;
-        if (j < nvec) raw[i].load(xr + (size_t)j * kE);
-        else raw[i].zero();
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVpt; ++i) {
-        float f[kE];
-        raw[i].get(f);
-#pragma unroll
-        for (int u = 0; u < kE; ++u) s += f[u];
-    }
-    const float mu = row_sum<kTpr>(s, sred[0]) / float(N);
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVpt; ++i) {
-        if (t + i * kTpr >= nvec) break;
-        float f[kE];
-        raw[i].get(f);
-#pragma unroll
-        for (int u = 0; u < kE; ++u) s += (f[u] - mu) * (f[u] - mu);
-    }
-    const float r = 1.f / sqrtf(row_sum<kTpr>(s, sred[1]) / float(N) + eps);
-    if (t == 0) {
-        if (mean) mean[row] = mu;
-        if (rstd) rstd[row] = r;
-    }
-    T* yr = y + row * ldy;
-#pragma unroll
-    for (int i = 0; i < kVpt; ++i) {
-        const int j = t + i * kTpr;
-        if (j >= nvec) break;
-        float f[kE];
-        raw[i].get(f);
-#pragma unroll
-        for (int u = 0; u < kE; u += 4) {
-            const float4 ww = w ? *reinterpret_cast<const float4*>(w + (size_t)j * kE + u) : make_float4(1, 1, 1, 1);
-            const float4 bb = b ? *reinterpret_cast<const float4*>(b + (size_t)j * kE + u) : make_float4(0, 0, 0, 0);
-            f[u] = (f[u] - mu) * r * ww.x + bb.x;
-            f[u + 1] = (f[u + 1] - mu) * r * ww.y + bb.y;
-            f[u + 2] = (f[u + 2] - mu) * r * ww.z + bb.z;
-            f[u + 3] = (f[u + 3] - mu) * r * ww.w + bb.w;
+        for (int i = 0; i < kVpt; ++i) {
+            const int j = t + i * kTpr;
+            if (j < nvec) raw[i].load_stream(x + row * ldx + (size_t)j * kE);
+            else raw[i].zero();
         }
-        raw[i].set(f);
-        raw[i].store(yr + (size_t)j * kE);
+        f2 f[kVpt][kE / 2], sum = 0ull;
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            pairs(raw[i], f[i]);
+#pragma unroll
+            for (int u = 0; u < kE / 2; ++u) sum = add2(sum, f[i][u]);
+        }
+        const float mu = row_sum<kTpr>(lo2(sum) + hi2(sum), sred[0]) / float(N);
+        const f2 nmu = dup2(-mu);
+        sum = 0ull;
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            if (t + i * kTpr >= nvec) break;
+#pragma unroll
+            for (int u = 0; u < kE / 2; ++u) {
+                f[i][u] = add2(f[i][u], nmu);
+                sum = fma2(f[i][u], f[i][u], sum);
+            }
+        }
+        const float r = 1.f / sqrtf(row_sum<kTpr>(lo2(sum) + hi2(sum), sred[1]) / float(N) + eps);
+        if (t == 0) {
+            if (mean) mean[row] = mu;
+            if (rstd) rstd[row] = r;
+        }
+        T* yr = y + row * ldy;
+        const f2 r2 = dup2(r);
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            const int j = t + i * kTpr;
+            if (j >= nvec) break;
+            float o[kE];
+#pragma unroll
+            for (int u = 0; u < kE; u += 4) {
+                f2 v0 = mul2(f[i][u / 2], r2), v1 = mul2(f[i][u / 2 + 1], r2);
+                if (w) {
+                    const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(w + (size_t)j * kE + u);
+                    const ulonglong2 bb = b ? *reinterpret_cast<const ulonglong2*>(b + (size_t)j * kE + u) : make_ulonglong2(0, 0);
+                    v0 = fma2(v0, ww.x, bb.x);
+                    v1 = fma2(v1, ww.y, bb.y);
+                } else if (b) {
+                    const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(b + (size_t)j * kE + u);
+                    v0 = add2(v0, bb.x);
+                    v1 = add2(v1, bb.y);
+                }
+                upk(v0, o[u], o[u + 1]);
+                upk(v1, o[u + 2], o[u + 3]);
+            }
+            raw[i].set(o);
+            raw[i].store(yr + (size_t)j * kE);
+        }
+    }
+}
+
+// Many rows of up to 512 vectors: kTpr threads own two vectors of columns each and keep
+// those columns' weight and bias in registers for all the rows that the block walks
+// (read from L1 for every row they are four times the row's own bytes, and the L1 pipe
+// was the bound: 102 us at 65536 x 2048 bf16, now 90 us = 6.0 TB/s).  512 threads an SM
+// measured best (384: 98, 640: 97, 768: 122 us).  kR rows at a time share the barriers;
+// the rows to come are on their way into a ring by copies that each thread waits for on
+// its own (it reads back only what it copied itself).
+template <typename T, int kTpr>
+__global__ void __launch_bounds__(kTpr)
+    fwd_rows_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ b,
+                    T* __restrict__ y, long long ldy, float* __restrict__ mean, float* __restrict__ rstd, int M, int N,
+                    float eps) {
+    constexpr int kE = Pack<T, true>::kN, kVpt = 2, kR = 2, kDepth = kTpr < 256 ? 3 : 2, kW = kTpr / 32;
+    __shared__ float sred[2][2][kW][kR];
+    __shared__ __align__(16) uint4 ring[kDepth][kR][kVpt][kTpr];
+    const int t = threadIdx.x, nvec = N / kE, warp = t >> 5;
+    const bool have[kVpt] = {t < nvec, t + kTpr < nvec};
+    f2 wv[kVpt][kE / 2], bv[kVpt][kE / 2];
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i)
+#pragma unroll
+        for (int u = 0; u < kE / 2; ++u) {
+            const int c = (t + i * kTpr) * kE + 2 * u;
+            wv[i][u] = w && have[i] ? pk(w[c], w[c + 1]) : dup2(1.f);
+            bv[i][u] = b && have[i] ? pk(b[c], b[c + 1]) : 0ull;
+        }
+    const long long step = (long long)gridDim.x * kR;
+    auto request = [&](long long r0, int slot) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int i = 0; i < kVpt; ++i)
+                if (r0 + r < M && have[i]) cp_async<16>(&ring[slot][r][i][t], x + (r0 + r) * ldx + (size_t)(t + i * kTpr) * kE);
+        cp_async_commit();
+    };
+    long long row = (long long)blockIdx.x * kR;
+#pragma unroll
+    for (int k = 0; k < kDepth - 1; ++k) request(row + k * step, k);
+    int slot = 0, buf = 0;
+    for (; row < M; row += step, buf ^= 1) {
+        cp_async_wait<kDepth - 2>();
+        f2 f[kR][kVpt][kE / 2];
+        float s[kR];
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            f2 a = 0ull;
+#pragma unroll
+            for (int i = 0; i < kVpt; ++i) {
+                Raw<T, true> raw;
+                if (row + r < M && have[i]) raw.v = ring[slot][r][i][t];
+                else raw.zero();
+                pairs(raw, f[r][i]);
+#pragma unroll
+                for (int u = 0; u < kE / 2; ++u) a = add2(a, f[r][i][u]);
+            }
+            s[r] = lo2(a) + hi2(a);
+        }
+        request(row + (kDepth - 1) * step, slot == 0 ? kDepth - 1 : slot - 1);  // into the place used before this one
+        if (++slot == kDepth) slot = 0;
+        // (the two sums have buffers of their own, and a row's barriers come before its
+        // successor but one writes them again)
+        auto block_sum = [&](int which) {
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+                if ((t & 31) == 0) sred[which][buf][warp][r] = s[r];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                s[r] = 0.f;
+#pragma unroll
+                for (int k = 0; k < kW; ++k) s[r] += sred[which][buf][k][r];
+            }
+        };
+        block_sum(0);
+        float mu[kR];
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            mu[r] = s[r] / float(N);
+            const f2 nmu = dup2(-mu[r]);
+            f2 a = 0ull;
+#pragma unroll
+            for (int i = 0; i < kVpt; ++i)
+                if (have[i]) {
+#pragma unroll
+                    for (int u = 0; u < kE / 2; ++u) {
+                        f[r][i][u] = add2(f[r][i][u], nmu);
+                        a = fma2(f[r][i][u], f[r][i][u], a);
+                    }
+                }
+            s[r] = lo2(a) + hi2(a);
+        }
+        block_sum(1);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            if (row + r >= M) break;
+            const float rs = 1.f / sqrtf(s[r] / float(N) + eps);
+            if (t == 0) {
+                if (mean) mean[row + r] = mu[r];
+                if (rstd) rstd[row + r] = rs;
+            }
+            const f2 r2 = dup2(rs);
+#pragma unroll
+            for (int i = 0; i < kVpt; ++i) {
+                float o[kE];
+#pragma unroll
+                for (int u = 0; u < kE / 2; ++u) upk(fma2(mul2(f[r][i][u], r2), wv[i][u], bv[i][u]), o[2 * u], o[2 * u + 1]);
+                Raw<T, true> raw;
+                raw.set(o);
+                if (have[i]) raw.store(y + (row + r) * ldy + (size_t)(t + i * kTpr) * kE);
+            }
+        }
     }
 }
 
@@ -136,11 +271,27 @@ __global__ void __launch_bounds__(kTpr)
     constexpr int kE = Pack<T, true>::kN;
     __shared__ float2 sred[2][kTpr / 32];
     const int t = threadIdx.x, nvec = N / kE;
-    float aw[kVpt][kE], ab[kVpt][kE];
+    // the columns' weights: in registers where they fit (16 a thread)
+    constexpr bool kHold = kVpt * kE <= 16;
+    f2 wv[kHold ? kVpt : 1][kE / 2];
+    if constexpr (kHold) {
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i)
+#pragma unroll
+            for (int u = 0; u < kE / 2; ++u) {
+                const int c = (t + i * kTpr) * kE + 2 * u;
+                wv[i][u] = w && t + i * kTpr < nvec ? pk(w[c], w[c + 1]) : dup2(1.f);
+            }
+    }
+    auto weights = [&](int i, int u) {
+        if constexpr (kHold) return make_ulonglong2(wv[i][u], wv[i][u + 1]);
+        else return w ? *reinterpret_cast<const ulonglong2*>(w + (t + i * kTpr) * kE + 2 * u) : make_ulonglong2(dup2(1.f), dup2(1.f));
+    };
+    f2 aw[kVpt][kE / 2], ab[kVpt][kE / 2];
 #pragma unroll
     for (int i = 0; i < kVpt; ++i)
 #pragma unroll
-        for (int u = 0; u < kE; ++u) aw[i][u] = ab[i][u] = 0.f;
+        for (int u = 0; u < kE / 2; ++u) aw[i][u] = ab[i][u] = 0ull;
     // the block's next row, requested one row ahead where the registers allow it (32
     // values a thread would spill)
     constexpr bool kAhead = kVpt * kE <= 16;
@@ -173,28 +324,29 @@ __global__ void __launch_bounds__(kTpr)
         }
         const float mu = nmu, r = nr;
         if (kAhead && row + gridDim.x < M) request(row + gridDim.x);
-        float s0 = 0.f, s1 = 0.f;
+        const f2 r2 = dup2(r), nmr = dup2(-mu * r);
+        f2 p0 = 0ull, p1 = 0ull;  // sums of c and c xh
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
             const int j = t + i * kTpr;
             if (j >= nvec) break;
-            float fx[kE], fd[kE];
-            rx[i].get(fx);
-            rd[i].get(fd);
+            f2 fx[kE / 2], fd[kE / 2];
+            pairs(rx[i], fx);
+            pairs(rd[i], fd);
 #pragma unroll
-            for (int u = 0; u < kE; u += 4) {
-                const float4 ww = w ? *reinterpret_cast<const float4*>(w + (size_t)j * kE + u) : make_float4(1, 1, 1, 1);
-                const float wv[4] = {ww.x, ww.y, ww.z, ww.w};
+            for (int u = 0; u < kE / 2; u += 2) {
+                const ulonglong2 ww = weights(i, u);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const float xh = (fx[u + v] - mu) * r, c = fd[u + v] * wv[v];
-                    s0 += c;
-                    s1 += c * xh;
-                    aw[i][u + v] += fd[u + v] * xh;
-                    ab[i][u + v] += fd[u + v];
+                for (int v = 0; v < 2; ++v) {
+                    const f2 xh = fma2(fx[u + v], r2, nmr), c = mul2(fd[u + v], v ? ww.y : ww.x);
+                    p0 = add2(p0, c);
+                    p1 = fma2(c, xh, p1);
+                    aw[i][u + v] = fma2(fd[u + v], xh, aw[i][u + v]);
+                    ab[i][u + v] = add2(ab[i][u + v], fd[u + v]);
                 }
             }
         }
+        float s0 = lo2(p0) + hi2(p0), s1 = lo2(p1) + hi2(p1);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             s0 += __shfl_xor_sync(0xffffffffu, s0, o);
@@ -210,26 +362,26 @@ __global__ void __launch_bounds__(kTpr)
             s0 += sred[buf][k].x;
             s1 += sred[buf][k].y;
         }
-        s0 /= float(N);
-        s1 /= float(N);
+        // dx = r c - r mean(c) - xh r mean(c xh)
+        const f2 m0 = dup2(-r * (s0 / float(N))), m1 = dup2(-r * (s1 / float(N)));
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
             const int j = t + i * kTpr;
             if (j >= nvec) break;
-            float fx[kE], fd[kE];
-            rx[i].get(fx);
-            rd[i].get(fd);
+            f2 fx[kE / 2], fd[kE / 2];
+            pairs(rx[i], fx);
+            pairs(rd[i], fd);
+            float o[kE];
 #pragma unroll
-            for (int u = 0; u < kE; u += 4) {
-                const float4 ww = w ? *reinterpret_cast<const float4*>(w + (size_t)j * kE + u) : make_float4(1, 1, 1, 1);
-                const float wv[4] = {ww.x, ww.y, ww.z, ww.w};
+            for (int u = 0; u < kE / 2; u += 2) {
+                const ulonglong2 ww = weights(i, u);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const float xh = (fx[u + v] - mu) * r;
-                    fd[u + v] = r * (fd[u + v] * wv[v] - s0 - xh * s1);
+                for (int v = 0; v < 2; ++v) {
+                    const f2 xh = fma2(fx[u + v], r2, nmr), c = mul2(fd[u + v], v ? ww.y : ww.x);
+                    upk(fma2(c, r2, fma2(xh, m1, m0)), o[2 * (u + v)], o[2 * (u + v) + 1]);
                 }
             }
-            rd[i].set(fd);
+            rd[i].set(o);
             rd[i].store(dx + row * lddx + (size_t)j * kE);
         }
     }
@@ -240,9 +392,9 @@ __global__ void __launch_bounds__(kTpr)
             if (j >= nvec) break;
             float* p = part + (size_t)blockIdx.x * 2 * N + (size_t)j * kE;
 #pragma unroll
-            for (int u = 0; u < kE; u += 4) {
-                *reinterpret_cast<float4*>(p + u) = make_float4(aw[i][u], aw[i][u + 1], aw[i][u + 2], aw[i][u + 3]);
-                *reinterpret_cast<float4*>(p + N + u) = make_float4(ab[i][u], ab[i][u + 1], ab[i][u + 2], ab[i][u + 3]);
+            for (int u = 0; u < kE / 2; u += 2) {
+                *reinterpret_cast<ulonglong2*>(p + 2 * u) = make_ulonglong2(aw[i][u], aw[i][u + 1]);
+                *reinterpret_cast<ulonglong2*>(p + N + 2 * u) = make_ulonglong2(ab[i][u], ab[i][u + 1]);
             }
         }
     }
@@ -326,17 +478,24 @@ int fwd(const T* x, long long ldx, const float* w, const float* b, T* y, long lo
     const long long lds[] = {ldx, ldy, 0, 0};
     const int nvec = N / kE;
     if (vec_ok(N, es, ptrs, lds, 4) && nvec <= 2048) {
-#define KDA_LN_FWD(TPR, VPT)                                                                                       \
-    fwd_kernel<T, TPR, VPT><<<unsigned(TPR >= 128 ? M : cdiv(M, 128 / TPR)), TPR > 128 ? TPR : 128, 0, st>>>(      \
+#define KDA_LN_FWD(TPR, VPT)                                                                                   \
+    fwd_kernel<T, TPR, VPT><<<unsigned(TPR == 32 ? cdiv(M, 4) : M), TPR == 32 ? 128 : TPR, 0, st>>>(           \
         x, ldx, w, b, y, ldy, mean, rstd, M, N, eps)
+#define KDA_LN_ROWS(TPR)                                                                                       \
+    fwd_rows_kernel<T, TPR><<<unsigned(device_sm_count()) * (512 / TPR), TPR, 0, st>>>(x, ldx, w, b, y, ldy, mean, \
+                                                                                       rstd, M, N, eps)
+        const bool many = M > 32 * device_sm_count();  // several rows for every block that the SMs hold
         if (nvec <= 32) KDA_LN_FWD(32, 1);
         else if (nvec <= 64) KDA_LN_FWD(32, 2);
+        else if (nvec <= 128 && many) KDA_LN_ROWS(64);
         else if (nvec <= 128) KDA_LN_FWD(32, 4);
-        else if (nvec <= 256 && M > 4 * device_sm_count()) KDA_LN_FWD(32, 8);
+        else if (nvec <= 256 && many) KDA_LN_ROWS(128);
         else if (nvec <= 256) KDA_LN_FWD(128, 2);
+        else if (nvec <= 512 && many) KDA_LN_ROWS(256);
         else if (nvec <= 512) KDA_LN_FWD(256, 2);
         else if (nvec <= 1024) KDA_LN_FWD(256, 4);
         else KDA_LN_FWD(512, 4);
+#undef KDA_LN_ROWS
 #undef KDA_LN_FWD
     } else {
         fwd_any_kernel<T><<<unsigned(M), 256, 0, st>>>(x, ldx, w, b, y, ldy, mean, rstd, N, eps);

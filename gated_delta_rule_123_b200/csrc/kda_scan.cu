@@ -118,7 +118,7 @@ __device__ __forceinline__ void load_states(VR<T, R>& r, const void* base, long 
     }
 }
 
-__device__ __forceinline__ float step_size(float raw, int softplus) { return softplus ? softplusf(raw) : raw; }
+__device__ __forceinline__ float step_size(float raw, int softplus) { return softplus ? softplus_poly(raw) : raw; }
 
 // R fp32 states of (row r of [..][N]) at n0; zero beyond N.
 template <int R>
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(32, 20) fwd_kernel(const SArgs a, bool bc_vec)
 }
 
 // One token per sequence, the state in place.  Bound by HBM: the state is read and
-// written once.  A quad of lanes holds one channel's states.
+// written once.  A quad of lanes holds one channel, R states a lane, for one sequence.
 template <typename T, int R, bool kFull>
 __global__ void __launch_bounds__(256) step_kernel(const SArgs a, float* __restrict__ state) {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -461,28 +461,23 @@ __global__ void __launch_bounds__(256) step_kernel(const SArgs a, float* __restr
     float h[R], A[R];
     if constexpr (kFull) {
         const VR<float, R> hv = *reinterpret_cast<const VR<float, R>*>(hp + n0);
-        const VR<float, R> av = *reinterpret_cast<const VR<float, R>*>(a.A + (size_t)d * a.N + n0);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            h[r] = hv.v[r];
-            A[r] = av.v[r];
-        }
+        for (int r = 0; r < R; ++r) h[r] = hv.v[r];
     } else {
         load_h<R>(h, hp, n0, a.N);
-        load_h<R>(A, a.A + (size_t)d * a.N, n0, a.N);
     }
+    load_h<R>(A, a.A + (size_t)d * a.N, n0, a.N);
+    VR<T, R> B, C;
+    load_states<T, R>(B, a.Bm, b * a.ldb + (long long)g * a.N, n0, a.N, kFull);
+    load_states<T, R>(C, a.Cm, b * a.ldc + (long long)g * a.N, n0, a.N, kFull);
     const float u = to_f32<T>(static_cast<const T*>(a.u)[b * a.ldu + d]);
     const float D = step_size(to_f32<T>(static_cast<const T*>(a.dt)[b * a.lddt + d]) + (a.bias ? a.bias[d] : 0.f),
                               a.softplus);
-    const T* Bp = static_cast<const T*>(a.Bm) + b * a.ldb + (long long)g * a.N;
-    const T* Cp = static_cast<const T*>(a.Cm) + b * a.ldc + (long long)g * a.N;
     float y = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const bool in = kFull || n0 + r < a.N;
-        const float Bv = in ? to_f32<T>(Bp[n0 + r]) : 0.f, Cv = in ? to_f32<T>(Cp[n0 + r]) : 0.f;
-        h[r] = ex2(D * A[r] * kL2e) * h[r] + D * u * Bv;
-        y += h[r] * Cv;
+        h[r] = ex2(D * A[r] * kL2e) * h[r] + D * u * to_f32<T>(B.v[r]);
+        y += h[r] * to_f32<T>(C.v[r]);
     }
     y += __shfl_xor_sync(0xffffffffu, y, 1);
     y += __shfl_xor_sync(0xffffffffu, y, 2);
@@ -497,11 +492,82 @@ __global__ void __launch_bounds__(256) step_kernel(const SArgs a, float* __restr
     }
     if (q == 0) {
         y += (a.skip ? a.skip[d] : 0.f) * u;
-        if (a.z) {
-            const float g2 = to_f32<T>(static_cast<const T*>(a.z)[b * a.ldz + d]);
-            y *= __fdividef(g2, 1.f + __expf(-g2));
-        }
+        if (a.z) y *= siluf(to_f32<T>(static_cast<const T*>(a.z)[b * a.ldz + d]));
         static_cast<T*>(a.y)[b * a.ldy + d] = from_f32<T>(y);
+    }
+}
+
+// The same for many sequences (whole 16-byte vectors of states): a thread keeps its
+// channel's A, bias and skip and walks the sequences b0 .. b1, the next kRing states on
+// their way into a ring that only it reads and the next sequence's other inputs in
+// registers.  256 x 4096 x 16 bf16: 25 us, against 42 us with a thread per sequence,
+// which has too few bytes in flight.
+template <typename T, int R>
+__global__ void __launch_bounds__(256) step_many_kernel(const SArgs a, float* __restrict__ state, int per) {
+    constexpr int kRing = 4;
+    using V = VR<float, R>;
+    __shared__ __align__(16) V ring[kRing][256];
+    const int tid = threadIdx.x;
+    const long long i = (long long)blockIdx.x * 256 + tid;
+    const int q = int(i & 3), n0 = q * R;
+    const bool live = (i >> 2) < a.D;
+    const int d = live ? int(i >> 2) : a.D - 1;  // (lanes past the last channel repeat it and store nothing)
+    const int g = d / a.Dg;
+    const int b0 = blockIdx.y * per, b1 = min(a.rows, b0 + per);
+    float A2[R];
+    load_h<R>(A2, a.A + (size_t)d * a.N, n0, a.N);
+#pragma unroll
+    for (int r = 0; r < R; ++r) A2[r] *= kL2e;
+    const float bias = a.bias ? a.bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
+    auto place = [&](int b) { return state + ((size_t)b * a.D + d) * a.N + n0; };
+    auto request = [&](int b, int slot) {
+        if (b < b1) {
+            constexpr int kB = sizeof(V) < 16 ? sizeof(V) : 16;
+#pragma unroll
+            for (int k = 0; k < int(sizeof(V)) / kB; ++k)
+                cp_async<kB>(reinterpret_cast<uint8_t*>(&ring[slot][tid]) + kB * k,
+                             reinterpret_cast<const uint8_t*>(place(b)) + kB * k);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kRing - 1; ++k) request(b0 + k, k);
+    T nu, ndt, nz = from_f32<T>(0.f);
+    VR<T, R> nB, nC;
+    auto load = [&](int b) {
+        nu = static_cast<const T*>(a.u)[b * a.ldu + d];
+        ndt = static_cast<const T*>(a.dt)[b * a.lddt + d];
+        if (a.z) nz = static_cast<const T*>(a.z)[b * a.ldz + d];
+        load_states<T, R>(nB, a.Bm, b * a.ldb + (long long)g * a.N, n0, a.N, true);
+        load_states<T, R>(nC, a.Cm, b * a.ldc + (long long)g * a.N, n0, a.N, true);
+    };
+    if (b0 < b1) load(b0);
+    int slot = 0;
+    for (int b = b0; b < b1; ++b) {
+        const float u = to_f32<T>(nu), raw = to_f32<T>(ndt) + bias, z = to_f32<T>(nz);
+        const VR<T, R> B = nB, C = nC;
+        if (b + 1 < b1) load(b + 1);
+        cp_async_wait<kRing - 2>();
+        V h = ring[slot][tid];
+        request(b + kRing - 1, slot == 0 ? kRing - 1 : slot - 1);  // the place of the state before this one
+        if (++slot == kRing) slot = 0;
+        const float D = step_size(raw, a.softplus), w = D * u;
+        float y = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            h.v[r] = ex2(D * A2[r]) * h.v[r] + w * to_f32<T>(B.v[r]);
+            y += h.v[r] * to_f32<T>(C.v[r]);
+        }
+        y += __shfl_xor_sync(0xffffffffu, y, 1);
+        y += __shfl_xor_sync(0xffffffffu, y, 2);
+        if (live) {
+            *reinterpret_cast<V*>(place(b)) = h;
+            if (q == 0) {
+                y += skip * u;
+                if (a.z) y *= siluf(z);
+                static_cast<T*>(a.y)[b * a.ldy + d] = from_f32<T>(y);
+            }
+        }
     }
 }
 
@@ -571,9 +637,17 @@ int fwd(const SArgs& a, cudaStream_t st) {
 
 template <typename T, int R>
 int step(const SArgs& a, float* state, cudaStream_t st) {
-    const unsigned grid = unsigned(cdiv((long long)a.rows * a.D * 4, 256));
-    if (a.N == 4 * R && al16(state) && al16(a.A)) step_kernel<T, R, true><<<grid, 256, 0, st>>>(a, state);
-    else step_kernel<T, R, false><<<grid, 256, 0, st>>>(a, state);
+    const bool full = al16(state) && states_ok(a, sizeof(T), R);
+    // blocks of the walking form: 4 an SM; it needs several sequences a block
+    const long long cols = cdiv((long long)a.D * 4, 256), splits = cdiv(4ll * device_sm_count(), cols);
+    if (full && a.rows >= 8 * splits) {
+        const int per = int(cdiv(a.rows, splits));
+        step_many_kernel<T, R><<<dim3(unsigned(cols), unsigned(cdiv(a.rows, per))), 256, 0, st>>>(a, state, per);
+    } else {
+        const unsigned grid = unsigned(cdiv((long long)a.rows * a.D * 4, 256));
+        if (full) step_kernel<T, R, true><<<grid, 256, 0, st>>>(a, state);
+        else step_kernel<T, R, false><<<grid, 256, 0, st>>>(a, state);
+    }
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -6,6 +6,7 @@ Every function checks shapes, types, strides and devices, allocates its outputs,
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -49,24 +50,31 @@ def _declare():
 _declare()
 
 
+_device_now = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_stream_of = (torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream")
+              else lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
 def _run(device, name, *args):
     """One library call with the tensors' device current, on that device's current stream."""
-    fn = getattr(_lib, name)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == _device_now():
+        rc = getattr(_lib, name)(*args, _stream_of(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(rc, name)
+            rc = getattr(_lib, name)(*args, _stream_of(index))
+    if rc:
+        _check(rc, name)
 
 
+@functools.lru_cache(maxsize=4096)
 def _query(device, name, *args):
-    """A workspace size for that device."""
-    if device.index == torch.cuda.current_device():
+    """A workspace size for that device (a function of the sizes alone)."""
+    if device.index == _device_now():
         return getattr(_lib, name)(*args)
     with torch.cuda.device(device):
         return getattr(_lib, name)(*args)
@@ -84,7 +92,7 @@ def _like(t, what, shape, dtype, device):
     """Check an operand against what the first one fixes; None passes."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
@@ -102,17 +110,16 @@ def _whole(t, what, shape, dtype, device):
 
 def _ld(t, what, inner=1):
     """Row stride of a tensor whose last ``inner`` axes are contiguous and whose leading axes form one axis of rows."""
-    shape, stride = t.shape, t.stride()
-    want = 1
-    if t.numel() == 0:  # no rows to step over
-        for k in range(1, inner + 1):
-            want *= shape[-k]
+    shape = t.shape
+    want = shape[-1] if inner == 1 else shape[-1] * shape[-2]
+    numel = t.numel()
+    if numel <= want:  # no rows to step over: any stride does
+        _ld_inner(t, what, inner)
         return (want + 7) // 8 * 8
-    for k in range(1, inner + 1):
-        if shape[-k] != 1 and stride[-k] != want:
-            raise ValueError(f"{what}: the last {inner} axes must be contiguous")
-        want *= shape[-k]
-    ld = None
+    if t.is_contiguous():
+        return want
+    _ld_inner(t, what, inner)
+    stride, ld, rows = t.stride(), None, 1
     for k in range(len(shape) - inner - 1, -1, -1):
         if shape[k] == 1:
             continue
@@ -122,11 +129,17 @@ def _ld(t, what, inner=1):
             raise ValueError(f"{what}: rows of the leading axes must be evenly spaced")
         else:
             rows *= shape[k]
-    if ld is None:  # a single row: any stride does
-        return (want + 7) // 8 * 8
     if ld < want:
         raise ValueError(f"{what}: rows must not overlap")
     return ld
+
+
+def _ld_inner(t, what, inner):
+    shape, stride, step = t.shape, t.stride(), 1
+    for k in range(1, inner + 1):
+        if shape[-k] > 1 and stride[-k] != step:
+            raise ValueError(f"{what}: the last {inner} axes must be contiguous")
+        step *= shape[-k]
 
 
 def _scratch(workspace, need, device):
@@ -148,6 +161,11 @@ def _seqs(cu_seqlens, B, device):
     return cu_seqlens.numel() - 1, cu_seqlens.numel() - 1
 
 
+def _new(like):
+    """An output of that shape and type, contiguous."""
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
+
+
 # ---------------------------------------------------------------- layer norm
 def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
     """Layer norm over the last axis (``kda_layer_norm_fwd``).  x [..., N] bf16 or fp32; weight, bias fp32 [N] or None.
@@ -157,8 +175,9 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
     N, lead = x.shape[-1], x.shape[:-1]
     _whole(weight, "weight", (N,), torch.float32, dev)
     _whole(bias, "bias", (N,), torch.float32, dev)
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else _like(out, "out", x.shape, x.dtype, dev)
-    mean, rstd = torch.empty((2, *lead), device=dev, dtype=torch.float32).unbind(0)
+    y = _new(x) if out is None else _like(out, "out", x.shape, x.dtype, dev)
+    mean = torch.empty(lead, device=dev, dtype=torch.float32)
+    rstd = torch.empty_like(mean)
     M = mean.numel()
     _run(dev, "kda_layer_norm_fwd", _p(x), _ld(x, "x"), _p(weight), _p(bias), _p(y), _ld(y, "out"), _p(mean), _p(rstd), M,
          N, _CODE[x.dtype], float(eps))
@@ -175,7 +194,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, weight_grad=True, bias_grad=True, 
     _whole(mean, "mean", lead, torch.float32, dev)
     _whole(rstd, "rstd", lead, torch.float32, dev)
     M = mean.numel()
-    dx = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    dx = _new(x)
     dw = torch.empty(N, device=dev, dtype=torch.float32) if weight_grad else None
     db = torch.empty(N, device=dev, dtype=torch.float32) if bias_grad else None
     ws, n = _scratch(workspace, _query(dev, "kda_layer_norm_bwd_workspace", M, N), dev)
@@ -259,7 +278,7 @@ def short_conv_fwd(x, weight, bias=None, cu_seqlens=None, conv_state=None, silu=
 
     Returns (y, conv_state after the call or None)."""
     dev, B, T, C, W, nseq, n = _conv_operands(x, weight, bias, cu_seqlens, conv_state)
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else _like(out, "out", x.shape, x.dtype, dev)
+    y = _new(x) if out is None else _like(out, "out", x.shape, x.dtype, dev)
     cs = _whole(conv_state_out, "conv_state_out", (n, W - 1, C), x.dtype, dev)
     if cs is None and output_conv_state:
         cs = torch.empty((n, W - 1, C), device=dev, dtype=x.dtype)
@@ -275,7 +294,7 @@ def short_conv_bwd(dy, x, weight, bias=None, cu_seqlens=None, conv_state=None, d
     dev, B, T, C, W, nseq, n = _conv_operands(x, weight, bias, cu_seqlens, conv_state)
     _like(dy, "dy", x.shape, x.dtype, dev)
     _whole(d_conv_state_out, "d_conv_state_out", (n, W - 1, C), x.dtype, dev)
-    dx = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    dx = _new(x)
     dw = torch.empty((C, W), device=dev, dtype=x.dtype)
     db = torch.empty(C, device=dev, dtype=torch.float32)
     dc = torch.empty((n, W - 1, C), device=dev, dtype=x.dtype) if conv_state is not None else None
@@ -297,7 +316,7 @@ def short_conv_step(x, weight, conv_state, bias=None, silu=True, out=None):
     _whole(weight, "weight", (C, W), x.dtype, dev)
     _whole(bias, "bias", (C,), torch.float32, dev)
     _whole(conv_state, "conv_state", (B, W - 1, C), x.dtype, dev)
-    y = torch.empty((B, C), device=dev, dtype=x.dtype) if out is None else _like(out, "out", x.shape, x.dtype, dev)
+    y = _new(x) if out is None else _like(out, "out", x.shape, x.dtype, dev)
     _run(dev, "kda_short_conv_step", _p(x), _ld(x, "x"), _p(weight), _p(bias), _p(conv_state), _p(y), _ld(y, "out"), B, C, W,
          _CODE[x.dtype], int(silu))
     return y
@@ -340,7 +359,7 @@ def selective_scan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     fs = _whole(final_state, "final_state", (n, ch, N), torch.float32, dev)
     if fs is None and output_final_state:
         fs = torch.empty((n, ch, N), device=dev, dtype=torch.float32)
-    y = torch.empty(u.shape, device=dev, dtype=u.dtype) if out is None else _like(out, "out", u.shape, u.dtype, dev)
+    y = _new(u) if out is None else _like(out, "out", u.shape, u.dtype, dev)
     ws, size = _scratch(workspace, _query(dev, "kda_selective_scan_fwd_workspace", nb, T, ch, G, N, nseq), dev)
     _run(dev, "kda_selective_scan_fwd", *args, _p(initial_state), _p(fs), _p(y), _ld(y, "out"), _p(cu_seqlens), nseq, nb, T,
          _CODE[u.dtype], _p(ws), size)
@@ -361,9 +380,9 @@ def selective_scan_bwd(dy, u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
     _like(dy, "dy", u.shape, u.dtype, dev)
     _whole(initial_state, "initial_state", (n, ch, N), torch.float32, dev)
     _whole(d_final_state, "d_final_state", (n, ch, N), torch.float32, dev)
-    du, ddt = (torch.empty(u.shape, device=dev, dtype=u.dtype) for _ in range(2))
-    dz = torch.empty(u.shape, device=dev, dtype=u.dtype) if z is not None else None
-    dB, dC = (torch.empty(B.shape, device=dev, dtype=u.dtype) for _ in range(2))
+    du, ddt = (_new(u) for _ in range(2))
+    dz = _new(u) if z is not None else None
+    dB, dC = (_new(B) for _ in range(2))
     dA = torch.empty((ch, N), device=dev, dtype=torch.float32)
     dD = torch.empty(ch, device=dev, dtype=torch.float32) if D is not None else None
     db = torch.empty(ch, device=dev, dtype=torch.float32) if dt_bias is not None else None
@@ -382,6 +401,6 @@ def selective_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
         raise ValueError("u [B, channels] must have two axes")
     dev, ch, G, N, params, args = _scan_operands(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
     _whole(state, "state", (u.shape[0], ch, N), torch.float32, dev)
-    y = torch.empty(u.shape, device=dev, dtype=u.dtype) if out is None else _like(out, "out", u.shape, u.dtype, dev)
+    y = _new(u) if out is None else _like(out, "out", u.shape, u.dtype, dev)
     _run(dev, "kda_selective_scan_step", *args, _p(state), _p(y), _ld(y, "out"), u.shape[0], _CODE[u.dtype])
     return y
