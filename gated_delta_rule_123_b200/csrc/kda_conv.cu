@@ -191,7 +191,7 @@ __device__ __forceinline__ float dsilu(float s) {
 // its whole gradient.  The run's sums for dw and db stay in registers and are
 // written as partial sums [run][W + 1][C].
 template <typename T, int W, bool kVec>
-__global__ void __launch_bounds__(128, Pack<T, kVec>::kN == 8 ? 2 : (Pack<T, kVec>::kN == 4 ? 4 : 8))
+__global__ void __launch_bounds__(128, Pack<T, kVec>::kN == 8 ? 2 : (Pack<T, kVec>::kN == 4 ? 3 : 8))
     bwd_kernel(const Args a, int run) {
     constexpr int kE = Pack<T, kVec>::kN;
     const int c0 = (blockIdx.y * 128 + threadIdx.x) * kE;
@@ -478,7 +478,7 @@ static int fwd_run(int ntok, int C, int kE) {
 
 // The same for the backward pass, whose registers bound the blocks of an SM; also what the
 // runs' partial sums cost, (W + 1) x 4 bytes per channel and run.
-__host__ __device__ constexpr int bwd_blocks(int kE) { return kE == 8 ? 2 : (kE == 4 ? 4 : 8); }
+__host__ __device__ constexpr int bwd_blocks(int kE) { return kE == 8 ? 2 : (kE == 4 ? 3 : 8); }
 static int bwd_run(int ntok, int C, int kE) {
     const long long want = cdiv((long long)ntok * cdiv(cdiv(C, kE), 128), (long long)device_sm_count() * bwd_blocks(kE));
     return int(want < 16 ? 16 : want);

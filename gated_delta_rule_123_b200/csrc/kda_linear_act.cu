@@ -464,19 +464,29 @@ __device__ __forceinline__ float act1(float x, int act) {
 }
 
 // Few rows of x (decode): bound by reading W once.  A block has 16 rows of W (outputs);
-// its 16 warps take slices of K and add their sums in shared memory, in order.  Warp
-// MMAs (m16n8k16) with W as the 16-row operand and up to 8 kMT rows of x as columns: the
-// sum over k has no order, so a thread's fragments are 8 neighbouring values of its
-// rows, and W goes from memory to registers in 16-byte loads, without shared memory.
-// 16 x 2048 x 4096: 5.4 us; 128-row tiles of the kernel above leave most SMs idle and
-// 112 of 128 rows empty (32 us).
-constexpr int kSkinnyWarps = 16;
+// its warps take slices of K and add their sums in shared memory, in order.  Warp MMAs
+// (m16n8k16) with W as the 16-row operand and up to 8 kMT rows of x as columns: the sum
+// over k has no order, so a thread's fragments are 8 neighbouring values of its rows,
+// 16 bytes that it copies into a ring of kU steps and reads back itself, with no
+// exchange between threads.  (Loads into registers do not stay in flight: the compiler
+// sinks them to their MMAs, 54 registers where kU steps would need 96.)  128-row tiles of
+// the kernel above leave most SMs idle and 112 of 128 rows empty: 32 us at 16 x 2048 x 4096.
+constexpr int kSkinnyWarps = 8;
+template <int kMT>
+struct Skinny {
+    static constexpr int kU = kMT <= 2 ? 6 : (kMT == 4 ? 4 : 3), kV = 2 + kMT;  // steps in flight; vectors a thread copies per step
+    static constexpr int kRing = kSkinnyWarps * kU * kV * 32 * 16, kRed = kSkinnyWarps * 16 * (8 * kMT + 1) * 4;
+    static constexpr int kSmem = kRing > kRed ? kRing : kRed;  // (the sums reuse the ring)
+};
+
 template <int kMT>
 __global__ void __launch_bounds__(32 * kSkinnyWarps)
     skinny_kernel(const __nv_bfloat16* __restrict__ x, int ldx, const __nv_bfloat16* __restrict__ W, int ldw,
                   const LArgs p) {
-    __shared__ float red[kSkinnyWarps][16][8 * kMT + 1];
+    constexpr int kU = Skinny<kMT>::kU, kV = Skinny<kMT>::kV;
+    extern __shared__ __align__(16) uint8_t skinny_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    uint4* ring = reinterpret_cast<uint4*>(skinny_smem) + (size_t)warp * kU * kV * 32 + lane;
     const int n0 = blockIdx.x * 16;
     // K in steps of 32 (8 values a thread), dealt to the warps in runs
     const int steps = (p.K + 31) / 32, per = (steps + kSkinnyWarps - 1) / kSkinnyWarps;
@@ -488,35 +498,50 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps)
         for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
     const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N;
     const __nv_bfloat16 *w0 = W + (size_t)(n0 + g) * ldw, *w1 = W + (size_t)(n0 + g + 8) * ldw;
-    constexpr int kU = kMT == 1 ? 8 : (kMT == 2 ? 6 : 4);  // steps in flight, of W and of x: what the registers hold
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int sb = s0; sb < s1; sb += kU) {
-        uint4 a0[kU], a1[kU], b[kU][kMT];
-#pragma unroll
-        for (int i = 0; i < kU; ++i) {
-            const int k = (sb + i) * 32 + t * 8;
-            const bool in = sb + i < s1 && k < p.K;
-            a0[i] = in && in0 ? __ldcs(reinterpret_cast<const uint4*>(w0 + k)) : zero;
-            a1[i] = in && in1 ? __ldcs(reinterpret_cast<const uint4*>(w1 + k)) : zero;
-#pragma unroll
-            for (int m = 0; m < kMT; ++m)
-                b[i][m] = in && m * 8 + g < p.M ? __ldg(reinterpret_cast<const uint4*>(x + (size_t)(m * 8 + g) * ldx + k)) : zero;
-        }
-#pragma unroll
-        for (int i = 0; i < kU; ++i) {
+    auto request = [&](int s, int slot) {
+        const int k = s * 32 + t * 8;
+        uint4* v = ring + slot * kV * 32;
+        if (s < s1) {
+            const bool in = k < p.K;  // (K is a multiple of 8)
+            if (in && in0) mix::cp_async<16>(v, w0 + k);
+            else v[0] = zero;
+            if (in && in1) mix::cp_async<16>(v + 32, w1 + k);
+            else v[32] = zero;
 #pragma unroll
             for (int m = 0; m < kMT; ++m) {
-                asm volatile(
-                    "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                    : "+f"(acc[m][0]), "+f"(acc[m][1]), "+f"(acc[m][2]), "+f"(acc[m][3])
-                    : "r"(a0[i].x), "r"(a1[i].x), "r"(a0[i].y), "r"(a1[i].y), "r"(b[i][m].x), "r"(b[i][m].y));
-                asm volatile(
-                    "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                    : "+f"(acc[m][0]), "+f"(acc[m][1]), "+f"(acc[m][2]), "+f"(acc[m][3])
-                    : "r"(a0[i].z), "r"(a1[i].z), "r"(a0[i].w), "r"(a1[i].w), "r"(b[i][m].z), "r"(b[i][m].w));
+                if (in && m * 8 + g < p.M) mix::cp_async<16>(v + (2 + m) * 32, x + (size_t)(m * 8 + g) * ldx + k);
+                else v[(2 + m) * 32] = zero;
             }
         }
+        mix::cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kU - 1; ++i) request(s0 + i, i);
+    int slot = 0;
+    for (int s = s0; s < s1; ++s) {
+        mix::cp_async_wait<kU - 2>();
+        const uint4* v = ring + slot * kV * 32;
+        const uint4 a0 = v[0], a1 = v[32];
+        uint4 b[kMT];
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) b[m] = v[(2 + m) * 32];
+        request(s + kU - 1, slot == 0 ? kU - 1 : slot - 1);  // into the place of the step before this one
+        if (++slot == kU) slot = 0;
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+            asm volatile(
+                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                : "+f"(acc[m][0]), "+f"(acc[m][1]), "+f"(acc[m][2]), "+f"(acc[m][3])
+                : "r"(a0.x), "r"(a1.x), "r"(a0.y), "r"(a1.y), "r"(b[m].x), "r"(b[m].y));
+            asm volatile(
+                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                : "+f"(acc[m][0]), "+f"(acc[m][1]), "+f"(acc[m][2]), "+f"(acc[m][3])
+                : "r"(a0.z), "r"(a1.z), "r"(a0.w), "r"(a1.w), "r"(b[m].z), "r"(b[m].w));
+        }
     }
+    __syncthreads();  // every warp has used its ring
+    float (*red)[16][8 * kMT + 1] = reinterpret_cast<float (*)[16][8 * kMT + 1]>(skinny_smem);
 #pragma unroll
     for (int m = 0; m < kMT; ++m) {  // sums: rows g, g + 8 of W; columns (rows of x) 2t, 2t + 1
         red[warp][g][m * 8 + 2 * t] = acc[m][0];
@@ -541,7 +566,11 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps)
 template <int kMT>
 static int launch_skinny(const void* x, int ldx, const void* W, int ldw, const LArgs& a, cudaStream_t st,
                          const char** why) {
-    skinny_kernel<kMT><<<unsigned(mix::cdiv(a.N, 16)), 32 * kSkinnyWarps, 0, st>>>(
+    if (!set_smem_attr(skinny_kernel<kMT>, Skinny<kMT>::kSmem)) {
+        *why = "cudaFuncSetAttribute failed for the skinny kernel";
+        return KDA_ERR_CUDA;
+    }
+    skinny_kernel<kMT><<<unsigned(mix::cdiv(a.N, 16)), 32 * kSkinnyWarps, Skinny<kMT>::kSmem, st>>>(
         static_cast<const __nv_bfloat16*>(x), ldx, static_cast<const __nv_bfloat16*>(W), ldw, a);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) return KDA_OK;
@@ -585,23 +614,35 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int u = 0; u < kE; ++u) sum[u] = 0.f;
     if (c0 < N) {
-#pragma unroll 4
-        for (long long r = r0 + ty; r < r1; r += 8) {
-            V vd, vs;
-            float d[kE], x[kE];
-            vd.load(dy + r * lddy + c0);
-            if (act != kNone) vs.load(s + r * lds + c0);
-            vd.get(d);
-            if (act != kNone) {
-                vs.get(x);
+        // four rows' loads before the first is used
+        constexpr int kU = 4;
+        for (long long rb = r0 + ty; rb < r1; rb += 8 * kU) {
+            V vd[kU], vs[kU];
 #pragma unroll
-                for (int u = 0; u < kE; ++u) d[u] *= dact(x[u], act);
+            for (int i = 0; i < kU; ++i) {
+                const long long r = rb + 8 * i;
+                if (r < r1) {
+                    vd[i].load_stream(dy + r * lddy + c0);
+                    if (act != kNone) vs[i].load_stream(s + r * lds + c0);
+                }
             }
 #pragma unroll
-            for (int u = 0; u < kE; ++u) sum[u] += d[u];
-            if (ds) {
-                vd.set(d);
-                vd.store(ds + r * ldds + c0);
+            for (int i = 0; i < kU; ++i) {
+                const long long r = rb + 8 * i;
+                if (r >= r1) break;
+                float d[kE], x[kE];
+                vd[i].get(d);
+                if (act != kNone) {
+                    vs[i].get(x);
+#pragma unroll
+                    for (int u = 0; u < kE; ++u) d[u] *= dact(x[u], act);
+                }
+#pragma unroll
+                for (int u = 0; u < kE; ++u) sum[u] += d[u];
+                if (ds) {
+                    vd[i].set(d);
+                    vd[i].store(ds + r * ldds + c0);
+                }
             }
         }
     }
@@ -618,12 +659,10 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Rows per block of act_grad_kernel: a multiple of 8 that gives about four blocks an SM.
+// Rows per block of act_grad_kernel: a multiple of 32 that makes one wave of 2 blocks an SM.
 static int grad_rows(int M, int N, int kE) {
-    const long long cols = mix::cdiv(N, 32 * kE);
-    const long long want = mix::cdiv((long long)M * cols, (long long)device_sm_count() * 4);
-    const long long r = mix::cdiv(want, 8) * 8;
-    return int(r < 32 ? 32 : r);
+    const long long cols = mix::cdiv(N, 32 * kE), fit = (long long)device_sm_count() * 2 / cols;
+    return int(mix::cdiv(mix::cdiv(M, fit > 0 ? fit : 1), 32) * 32);
 }
 
 }  // namespace lin
@@ -640,14 +679,17 @@ int launch_linear_act(const void* x, int ldx, const void* W, int ldw, const floa
     a.ldr = ldr;
     a.res_vec = res && mix::al16(res) && ldr % 8 == 0;
     a.act = act;
-    if (M <= 32) {
+    // Up to 32 rows: the skinny kernel.  Up to 64 it pays while 64-wide tiles leave half of the
+    // SMs idle (64 x 2048 x 4096: 14 against 28 us; 64 x 8192 x 2048: 34 against 17 us).
+    if (M <= 32 || (M <= 64 && 2 * mix::cdiv(N, 64) <= device_sm_count())) {
         a.c = static_cast<__nv_bfloat16*>(y);
         a.ldc = ldy;
         a.pre = static_cast<__nv_bfloat16*>(pre);
         a.ldp = ldp;
         if (M <= 8) return lin::launch_skinny<1>(x, ldx, W, ldw, a, st, why);
         if (M <= 16) return lin::launch_skinny<2>(x, ldx, W, ldw, a, st, why);
-        return lin::launch_skinny<4>(x, ldx, W, ldw, a, st, why);
+        if (M <= 32) return lin::launch_skinny<4>(x, ldx, W, ldw, a, st, why);
+        return lin::launch_skinny<8>(x, ldx, W, ldw, a, st, why);
     }
     if (pre) return lin::launch<false, false, true>(x, ldx, W, ldw, y, ldy, pre, ldp, a, st, why);
     return lin::launch<false, false, false>(x, ldx, W, ldw, y, ldy, nullptr, 0, a, st, why);

@@ -519,37 +519,53 @@ __global__ void __launch_bounds__(256) step_many_kernel(const SArgs a, float* __
 #pragma unroll
     for (int r = 0; r < R; ++r) A2[r] *= kL2e;
     const float bias = a.bias ? a.bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
-    auto place = [&](int b) { return state + ((size_t)b * a.D + d) * a.N + n0; };
-    auto request = [&](int b, int slot) {
-        if (b < b1) {
+    const size_t row = (size_t)a.D * a.N;
+    float *ahead = state + b0 * row + (size_t)d * a.N + n0, *hp = ahead;  // the state to request next, and this one's
+    int left = b1 - b0;  // states still to request
+    auto request = [&](int slot) {
+        if (left > 0) {
             constexpr int kB = sizeof(V) < 16 ? sizeof(V) : 16;
 #pragma unroll
             for (int k = 0; k < int(sizeof(V)) / kB; ++k)
-                cp_async<kB>(reinterpret_cast<uint8_t*>(&ring[slot][tid]) + kB * k,
-                             reinterpret_cast<const uint8_t*>(place(b)) + kB * k);
+                cp_async<kB>(reinterpret_cast<uint8_t*>(&ring[slot][tid]) + kB * k, reinterpret_cast<uint8_t*>(ahead) + kB * k);
+            ahead += row;
+            --left;
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < kRing - 1; ++k) request(b0 + k, k);
+    for (int k = 0; k < kRing - 1; ++k) request(k);
+    // the other inputs of the next sequence, by pointers that step from one to the next
+    const T *pu = static_cast<const T*>(a.u) + b0 * a.ldu + d, *pd = static_cast<const T*>(a.dt) + b0 * a.lddt + d;
+    const T* pz = a.z ? static_cast<const T*>(a.z) + b0 * a.ldz + d : nullptr;
+    const T *pB = static_cast<const T*>(a.Bm) + b0 * a.ldb + (long long)g * a.N + n0;
+    const T *pC = static_cast<const T*>(a.Cm) + b0 * a.ldc + (long long)g * a.N + n0;
+    T* py = static_cast<T*>(a.y) + b0 * a.ldy + d;
     T nu, ndt, nz = from_f32<T>(0.f);
     VR<T, R> nB, nC;
-    auto load = [&](int b) {
-        nu = static_cast<const T*>(a.u)[b * a.ldu + d];
-        ndt = static_cast<const T*>(a.dt)[b * a.lddt + d];
-        if (a.z) nz = static_cast<const T*>(a.z)[b * a.ldz + d];
-        load_states<T, R>(nB, a.Bm, b * a.ldb + (long long)g * a.N, n0, a.N, true);
-        load_states<T, R>(nC, a.Cm, b * a.ldc + (long long)g * a.N, n0, a.N, true);
+    auto load = [&]() {
+        nu = *pu;
+        ndt = *pd;
+        if (pz) {
+            nz = *pz;
+            pz += a.ldz;
+        }
+        nB = *reinterpret_cast<const VR<T, R>*>(pB);
+        nC = *reinterpret_cast<const VR<T, R>*>(pC);
+        pu += a.ldu;
+        pd += a.lddt;
+        pB += a.ldb;
+        pC += a.ldc;
     };
-    if (b0 < b1) load(b0);
+    if (b0 < b1) load();
     int slot = 0;
     for (int b = b0; b < b1; ++b) {
         const float u = to_f32<T>(nu), raw = to_f32<T>(ndt) + bias, z = to_f32<T>(nz);
         const VR<T, R> B = nB, C = nC;
-        if (b + 1 < b1) load(b + 1);
+        if (b + 1 < b1) load();
         cp_async_wait<kRing - 2>();
         V h = ring[slot][tid];
-        request(b + kRing - 1, slot == 0 ? kRing - 1 : slot - 1);  // the place of the state before this one
+        request(slot == 0 ? kRing - 1 : slot - 1);  // into the place of the state before this one
         if (++slot == kRing) slot = 0;
         const float D = step_size(raw, a.softplus), w = D * u;
         float y = 0.f;
@@ -561,13 +577,15 @@ __global__ void __launch_bounds__(256) step_many_kernel(const SArgs a, float* __
         y += __shfl_xor_sync(0xffffffffu, y, 1);
         y += __shfl_xor_sync(0xffffffffu, y, 2);
         if (live) {
-            *reinterpret_cast<V*>(place(b)) = h;
+            *reinterpret_cast<V*>(hp) = h;
             if (q == 0) {
                 y += skip * u;
-                if (a.z) y *= siluf(z);
-                static_cast<T*>(a.y)[b * a.ldy + d] = from_f32<T>(y);
+                if (pz) y *= siluf(z);
+                *py = from_f32<T>(y);
             }
         }
+        hp += row;
+        py += a.ldy;
     }
 }
 
@@ -638,8 +656,8 @@ int fwd(const SArgs& a, cudaStream_t st) {
 template <typename T, int R>
 int step(const SArgs& a, float* state, cudaStream_t st) {
     const bool full = al16(state) && states_ok(a, sizeof(T), R);
-    // blocks of the walking form: 4 an SM; it needs several sequences a block
-    const long long cols = cdiv((long long)a.D * 4, 256), splits = cdiv(4ll * device_sm_count(), cols);
+    // blocks of the walking form: one wave of 4 an SM; it needs several sequences a block
+    const long long cols = cdiv((long long)a.D * 4, 256), fit = 4ll * device_sm_count() / cols, splits = fit > 1 ? fit : 1;
     if (full && a.rows >= 8 * splits) {
         const int per = int(cdiv(a.rows, splits));
         step_many_kernel<T, R><<<dim3(unsigned(cols), unsigned(cdiv(a.rows, per))), 256, 0, st>>>(a, state, per);
