@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -13,11 +14,12 @@ ROOT = os.path.dirname(HERE)
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
     "-Xptxas", "-v",
-    "--split-compile=0",  # the kernels of the one translation unit on all cores
 ]
+# translation units, compiled at the same time
+UNITS = ["kda_lib.cu", "kda_norm.cu", "kda_conv.cu", "kda_scan.cu", "kda_scan_bwd.cu"]
 
 
 def _sources():
@@ -36,18 +38,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
     nvcc = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [nvcc, *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp,
-           os.path.join(CSRC, "kda_lib.cu")]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("nvcc failed building libkda.so")
-    if verbose:
-        sys.stderr.write(res.stderr)
-    os.replace(tmp, LIB)
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, u + ".o") for u in UNITS]
+        runs = [subprocess.Popen([nvcc, *NVCC_FLAGS, "-c", "-I", os.path.join(ROOT, "include"), "-o", o, os.path.join(CSRC, u)],
+                                 stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for u, o in zip(UNITS, objs)]
+        logs = [r.communicate()[0] for r in runs]
+        for u, r, log in zip(UNITS, runs, logs):
+            if r.returncode != 0:
+                sys.stderr.write(log)
+                raise RuntimeError(f"nvcc failed building {u}")
+        if verbose:
+            sys.stderr.write("".join(logs))
+        lib = LIB + ".tmp%d" % os.getpid()
+        subprocess.run([nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", lib, *objs], check=True)
+        os.replace(lib, LIB)
     with open(os.path.join(HERE, "ptxas_info.txt"), "w") as f:
-        f.write(res.stderr)
+        f.write("".join(logs))
     return LIB
 
 

@@ -23,19 +23,19 @@ namespace kda {
 constexpr int kD = 128;      // head dim (d_k = d_v)
 constexpr int kC = 64;       // chunk length
 
-// Device-side status word (one per loaded library, per device).  Kernels OR
-// error bits in; kda_device_status() reads and clears it.  The library is one
-// translation unit (kda_lib.cu), so this is its only definition.
-__device__ int g_device_status = 0;
+// Device-side status word (per device).  Kernels OR error bits in;
+// kda_device_status() reads and clears it.  Every kernel that waits is in one
+// translation unit (kda_lib.cu), so that its copy is the only one in use.
+static __device__ int g_device_status = 0;
 
 // Bound of every device-side wait, in SM cycles: 2^31 by default (about a
 // second at the B200's clock).  kda_debug_fault_injection() lowers it for the
 // failure tests.
-__constant__ long long c_wait_limit = 1ll << 31;
+static __constant__ long long c_wait_limit = 1ll << 31;
 // Chunk (index inside a launch's sequence segment) whose q/k/g load the chunk
 // kernels' loader skips, or -1.  Set only by kda_debug_fault_injection() for
 // the failure tests: the bounded wait for the skipped load then gives up.
-__constant__ int c_skip_chunk_load = -1;
+static __constant__ int c_skip_chunk_load = -1;
 
 __device__ __forceinline__ void report_timeout(int where) {
     atomicOr(&g_device_status, 1 << (where & 15));

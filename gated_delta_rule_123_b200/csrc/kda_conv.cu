@@ -15,9 +15,45 @@
 
 namespace kda {
 
-namespace conv {  // seq_of and seq_begin (the sequence of a token, its first token) are the layer's
+namespace conv {
 
 using namespace mix;
+
+// Four channels of a row (8 bytes of bf16, 16 of fp32), or one.  (Eight bf16 channels a
+// thread need twice the registers: half the warps, or spills.)
+template <typename T, bool kVec>
+struct Row {
+    static constexpr int kN = kVec ? 4 : 1;
+    using type = typename std::conditional<kVec, typename std::conditional<sizeof(T) == 2, uint2, uint4>::type, T>::type;
+    type v;
+    __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const type*>(p); }
+    __device__ __forceinline__ void load_stream(const T* p) { v = __ldcs(reinterpret_cast<const type*>(p)); }
+    __device__ __forceinline__ void zero() {
+        if constexpr (!kVec) v = from_f32<T>(0.f);
+        else if constexpr (sizeof(T) == 2) v = make_uint2(0, 0);
+        else v = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float* f) const {
+        if constexpr (!kVec) {
+            f[0] = to_f32<T>(v);
+        } else if constexpr (sizeof(T) == 2) {
+            f[0] = __uint_as_float(v.x << 16);
+            f[1] = __uint_as_float(v.x & 0xffff0000u);
+            f[2] = __uint_as_float(v.y << 16);
+            f[3] = __uint_as_float(v.y & 0xffff0000u);
+        } else {
+            unpack16(v, f, 0.f);
+        }
+    }
+    __device__ __forceinline__ void set(const float* f) {
+        if constexpr (!kVec) v = from_f32<T>(f[0]);
+        else if constexpr (sizeof(T) == 2) v = make_uint2(pack2_rn(f[0], f[1]), pack2_rn(f[2], f[3]));
+        else v = pack16(f, 0.f);
+    }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<type*>(p) = v; }
+};
+
+constexpr int kFwdRing = 10, kFwdBlocks = 5;  // rows in flight a thread, blocks an SM
 
 struct Args {
     const void *x, *w, *cache_in;
@@ -64,7 +100,7 @@ __global__ void __launch_bounds__(256) tail_kernel(const Args a) {
 // The taps of a thread's channels: w[u][j], j = 0 the oldest.
 template <typename T, int W, int kE>
 __device__ __forceinline__ void load_taps(const T* w, int c0, float (&f)[kE][W]) {
-    if constexpr (kE > 1 && (W * sizeof(T)) % 8 == 0) {  // c0 is a multiple of kE: 16-byte aligned runs
+    if constexpr (kE > 1 && W == 4) {  // four channels' taps: 32 or 64 bytes in a row
         constexpr int kP = int(16 / sizeof(T));
 #pragma unroll
         for (int i = 0; i < kE * W / kP; ++i) {
@@ -81,19 +117,20 @@ __device__ __forceinline__ void load_taps(const T* w, int c0, float (&f)[kE][W])
     }
 }
 
-// A block: 128 vectors of channels (blockIdx.y) by a run of tokens (blockIdx.x).  A
-// thread keeps kRing rows in flight: each row's register is requested again, kRing
+// A thread: a vector of channels by a run of tokens (neighbouring threads, neighbouring
+// vectors; narrow channels put several runs into a block).  It keeps kRing rows in flight: each row's register is requested again, kRing
 // tokens ahead, as soon as its value has been used.
 template <typename T, int W, bool kVec, int kRing>
-__global__ void __launch_bounds__(128, 4) fwd_kernel(const Args a, int run) {
-    constexpr int kE = Pack<T, kVec>::kN, kP = kE > 1 ? kE / 2 : 1;
-    const int c0 = (blockIdx.y * 128 + threadIdx.x) * kE;
-    if (c0 >= a.C) return;
+__global__ void __launch_bounds__(128, kFwdBlocks) fwd_kernel(const Args a, int run) {
+    constexpr int kE = Row<T, kVec>::kN, kP = kE > 1 ? kE / 2 : 1;
+    const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
+    const int nvec = a.C / kE, at = int(id / nvec), c0 = int(id % nvec) * kE;
+    if ((long long)at * run >= a.ntok) return;
     const T* x = static_cast<const T*>(a.x) + c0;
     T* y = static_cast<T*>(a.y) + c0;
     const T* in = static_cast<const T*>(a.cache_in);
-    const int t0 = blockIdx.x * run, t1 = min(a.ntok, t0 + run);
-    Raw<T, kVec> ring[kRing];
+    const int t0 = at * run, t1 = min(a.ntok, t0 + run);
+    Row<T, kVec> ring[kRing];
 #pragma unroll
     for (int j = 0; j < kRing; ++j)
         if (t0 + j < t1) ring[j].load_stream(x + (long long)(t0 + j) * a.ldx);
@@ -110,7 +147,7 @@ __global__ void __launch_bounds__(128, 4) fwd_kernel(const Args a, int run) {
             b[u] = a.bias ? pk(a.bias[c0 + 2 * u * o], a.bias[c0 + 2 * u * o + o]) : 0ull;
         }
     }
-    auto get2 = [](const Raw<T, kVec>& r, f2 (&v)[kP]) {
+    auto get2 = [](const Row<T, kVec>& r, f2 (&v)[kP]) {
         float f[kE];
         r.get(f);
 #pragma unroll
@@ -122,7 +159,7 @@ __global__ void __launch_bounds__(128, 4) fwd_kernel(const Args a, int run) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int p = t - (W - 1) + j;
-            Raw<T, kVec> r;
+            Row<T, kVec> r;
             if (p >= s_beg) r.load(x + (long long)p * a.ldx);
             else if (in) r.load(in + ((size_t)n * (W - 1) + (W - 1 + p - s_beg)) * a.C + c0);
             else r.zero();
@@ -130,10 +167,14 @@ __global__ void __launch_bounds__(128, 4) fwd_kernel(const Args a, int run) {
         }
     };
     history(t0);
+    // the next row to request and the next one to store, stepped from token to token
+    const T* ahead = x + (long long)(t0 + kRing) * a.ldx;
+    T* out = y + (long long)t0 * a.ldy;
     auto token = [&](int i, int t) {
         f2 v[kP];
         get2(ring[i], v);
-        if (t + kRing < t1) ring[i].load_stream(x + (long long)(t + kRing) * a.ldx);
+        if (t + kRing < t1) ring[i].load_stream(ahead);
+        ahead += a.ldx;
         float o[kE];
 #pragma unroll
         for (int u = 0; u < kP; ++u) {
@@ -153,9 +194,10 @@ __global__ void __launch_bounds__(128, 4) fwd_kernel(const Args a, int run) {
             for (int j = 0; j + 1 < W - 1; ++j) h[j][u] = h[j + 1][u];
             h[W - 2][u] = v[u];
         }
-        Raw<T, kVec> r;
+        Row<T, kVec> r;
         r.set(o);
-        r.store(y + (long long)t * a.ldy);
+        r.store(out);
+        out += a.ldy;
     };
     for (int tb = t0; tb < t1; tb += kRing) {
         if (s_end >= tb + kRing && t1 >= tb + kRing && tb < s_end) {  // no edge in the ring: the window moves by renaming registers
@@ -186,22 +228,26 @@ __device__ __forceinline__ float dsilu(float s) {
     return g * (1.f + s * (1.f - g));
 }
 
+// Blocks of the backward pass that an SM's registers hold.
+__host__ __device__ constexpr int bwd_blocks(int kE) { return kE == 4 ? 3 : 8; }
+
 // Backward.  A thread slides over its run of tokens and W - 1 more: ds of a
 // token is formed once its window is complete, and the token W - 1 back then has
 // its whole gradient.  The run's sums for dw and db stay in registers and are
 // written as partial sums [run][W + 1][C].
 template <typename T, int W, bool kVec>
-__global__ void __launch_bounds__(128, Pack<T, kVec>::kN == 8 ? 2 : (Pack<T, kVec>::kN == 4 ? 3 : 8))
+__global__ void __launch_bounds__(128, bwd_blocks(Row<T, kVec>::kN))
     bwd_kernel(const Args a, int run) {
-    constexpr int kE = Pack<T, kVec>::kN;
-    const int c0 = (blockIdx.y * 128 + threadIdx.x) * kE;
-    if (c0 >= a.C) return;
+    constexpr int kE = Row<T, kVec>::kN;
+    const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
+    const int nvec = a.C / kE, at = int(id / nvec), c0 = int(id % nvec) * kE;
+    if ((long long)at * run >= a.ntok) return;
     const T* x = static_cast<const T*>(a.x) + c0;
     const T* dy = static_cast<const T*>(a.dy) + c0;
     T* dx = static_cast<T*>(a.dx) + c0;
     const T* in = static_cast<const T*>(a.cache_in);
     const T* dout = static_cast<const T*>(a.dcache_out);
-    const int t0 = blockIdx.x * run, t1 = min(a.ntok, t0 + run);
+    const int t0 = at * run, t1 = min(a.ntok, t0 + run);
     float w[kE][W], b[kE], aw[W][kE], ab[kE];
     load_taps<T, W, kE>(static_cast<const T*>(a.w), c0, w);
 #pragma unroll
@@ -219,7 +265,7 @@ __global__ void __launch_bounds__(128, Pack<T, kVec>::kN == 8 ? 2 : (Pack<T, kVe
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int p = t - (W - 1) + j;
-            Raw<T, kVec> r;
+            Row<T, kVec> r;
             if (p >= s_beg) r.load(x + (long long)p * a.ldx);
             else if (in) r.load(in + ((size_t)n * (W - 1) + (W - 1 + p - s_beg)) * a.C + c0);
             else r.zero();
@@ -236,21 +282,21 @@ __global__ void __launch_bounds__(128, Pack<T, kVec>::kN == 8 ? 2 : (Pack<T, kVe
 #pragma unroll
         for (int u = 0; u < kE; ++u) f[u] = v[u];
         if (dout && p >= s_end - (W - 1)) {
-            Raw<T, kVec> r;
+            Row<T, kVec> r;
             float e[kE];
             r.load(dout + ((size_t)n * (W - 1) + (p - (s_end - (W - 1)))) * a.C + c0);
             r.get(e);
 #pragma unroll
             for (int u = 0; u < kE; ++u) f[u] += e[u];
         }
-        Raw<T, kVec> r;
+        Row<T, kVec> r;
         r.set(f);
         r.store(dx + (long long)p * a.lddx);
     };
     history(t0);
     const int t2 = min(a.ntok, t1 + W - 1);
     constexpr int kRing = 4;  // rows in flight
-    Raw<T, kVec> nx[kRing], nd[kRing];
+    Row<T, kVec> nx[kRing], nd[kRing];
 #pragma unroll
     for (int j = 0; j < kRing; ++j)
         if (t0 + j < t2) {
@@ -287,7 +333,7 @@ __global__ void __launch_bounds__(128, Pack<T, kVec>::kN == 8 ? 2 : (Pack<T, kVe
             dn[u] = w[u][W - 1] * d[u];
         }
         if constexpr (decltype(whole)::value) {  // token t - (W - 1) is the run's and inside the sequence
-            Raw<T, kVec> r;
+            Row<T, kVec> r;
             r.set(g[0]);
             r.store(dx + (long long)(t - (W - 1)) * a.lddx);
         } else {
@@ -334,7 +380,7 @@ __global__ void __launch_bounds__(128, Pack<T, kVec>::kN == 8 ? 2 : (Pack<T, kVe
     }
     if (t2 == a.ntok && !done)  // the axis ends here: the last inputs have no later token
         for (int j = 0; j < W - 1; ++j) finish(t2 - (W - 1) + j, g[j]);
-    float* p = a.part + (size_t)blockIdx.x * (W + 1) * a.C + c0;
+    float* p = a.part + (size_t)at * (W + 1) * a.C + c0;
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
@@ -437,12 +483,12 @@ __global__ void __launch_bounds__(1024) bwd_finish_kernel(const Args a, int part
 // One token per sequence; the cache moves up one row in place.
 template <typename T, int W, bool kVec>
 __global__ void __launch_bounds__(128) step_kernel(const Args a, T* __restrict__ cache) {
-    constexpr int kE = Pack<T, kVec>::kN;
+    constexpr int kE = Row<T, kVec>::kN;
     const int nvec = a.C / kE;
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     if (i >= (long long)a.nseq * nvec) return;
     const int n = int(i / nvec), c0 = int(i % nvec) * kE;
-    Raw<T, kVec> h[W];
+    Row<T, kVec> h[W];
     T* cn = cache + (size_t)n * (W - 1) * a.C + c0;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) h[j].load(cn + (size_t)j * a.C);
@@ -467,29 +513,28 @@ __global__ void __launch_bounds__(128) step_kernel(const Args a, T* __restrict__
     h[0].store(static_cast<T*>(a.y) + n * a.ldy + c0);
 }
 
-constexpr int kFwdRing = 8;
 
-// Tokens of one thread in the forward pass: one wave of the 4 blocks that an SM holds.
-// (65536 x 4096 bf16: 443 tokens 190 us; 128 tokens, 3.5 waves, 224 us; 64 tokens 308 us.)
+// Tokens of one thread in the forward pass: one wave of the blocks that the SMs hold
+// (65536 x 4096 bf16 in 3.5 waves of shorter runs 224 us, in 7 waves 308 us, in one 194 us
+// = 5.5 TB/s).
 static int fwd_run(int ntok, int C, int kE) {
-    const long long want = cdiv((long long)ntok * cdiv(cdiv(C, kE), 128), (long long)device_sm_count() * 4);
+    const long long want = cdiv((long long)ntok * cdiv(C, kE), (long long)device_sm_count() * kFwdBlocks * 128);
     return int(want < 8 ? 8 : want);
 }
 
-// The same for the backward pass, whose registers bound the blocks of an SM; also what the
-// runs' partial sums cost, (W + 1) x 4 bytes per channel and run.
-__host__ __device__ constexpr int bwd_blocks(int kE) { return kE == 8 ? 2 : (kE == 4 ? 3 : 8); }
+// The same for the backward pass; long runs also write few partial sums, (W + 1) x 4 bytes
+// per channel and run.
 static int bwd_run(int ntok, int C, int kE) {
-    const long long want = cdiv((long long)ntok * cdiv(cdiv(C, kE), 128), (long long)device_sm_count() * bwd_blocks(kE));
-    return int(want < 16 ? 16 : want);
+    const long long want = cdiv((long long)ntok * cdiv(C, kE), (long long)device_sm_count() * bwd_blocks(kE) * 128);
+    return int(want < 8 ? 8 : want);
 }
 
 template <typename T, int W>
 int fwd(const Args& a, bool vec, cudaStream_t st) {
     if (a.ntok > 0) {
-        const int kE = vec ? int(16 / sizeof(T)) : 1;
+        const int kE = vec ? 4 : 1;
         const int run = fwd_run(a.ntok, a.C, kE);
-        const dim3 grid(unsigned(cdiv(a.ntok, run)), unsigned(cdiv(cdiv(a.C, kE), 128)));
+        const unsigned grid = unsigned(cdiv(cdiv(a.ntok, run) * (a.C / kE), 128));
         if (vec) fwd_kernel<T, W, true, kFwdRing><<<grid, 128, 0, st>>>(a, run);
         else fwd_kernel<T, W, false, kFwdRing><<<grid, 128, 0, st>>>(a, run);
     }
@@ -502,12 +547,12 @@ int fwd(const Args& a, bool vec, cudaStream_t st) {
 
 template <typename T, int W>
 int bwd(const Args& a, bool vec, void* dw, float* db, cudaStream_t st) {
-    const int kE = vec ? int(16 / sizeof(T)) : 1;
+    const int kE = vec ? 4 : 1;
     int parts = 0;
     if (a.ntok > 0) {
         const int run = bwd_run(a.ntok, a.C, kE);
         parts = int(cdiv(a.ntok, run));
-        const dim3 grid(parts, unsigned(cdiv(cdiv(a.C, kE), 128)));
+        const unsigned grid = unsigned(cdiv((long long)parts * (a.C / kE), 128));
         if (vec) bwd_kernel<T, W, true><<<grid, 128, 0, st>>>(a, run);
         else bwd_kernel<T, W, false><<<grid, 128, 0, st>>>(a, run);
     }
@@ -521,7 +566,7 @@ int bwd(const Args& a, bool vec, void* dw, float* db, cudaStream_t st) {
 
 template <typename T, int W>
 int step(const Args& a, bool vec, void* cache, cudaStream_t st) {
-    const int kE = vec ? int(16 / sizeof(T)) : 1;
+    const int kE = vec ? 4 : 1;
     const unsigned grid = unsigned(cdiv((long long)a.nseq * (a.C / kE), 128));
     if (vec) step_kernel<T, W, true><<<grid, 128, 0, st>>>(a, static_cast<T*>(cache));
     else step_kernel<T, W, false><<<grid, 128, 0, st>>>(a, static_cast<T*>(cache));
@@ -533,21 +578,22 @@ int step(const Args& a, bool vec, void* cache, cudaStream_t st) {
 size_t short_conv_bwd_workspace_bytes(int ntok, int C, int W) {
     // the shortest runs of any element type and alignment
     size_t parts = 0;
-    for (int e = 1; e <= 8; e *= 2) {
+    for (int e = 1; e <= 4; e += 3) {
         const size_t p = size_t(mix::cdiv(ntok, conv::bwd_run(ntok, C, e)));
         if (p > parts) parts = p;
     }
     return mix::up256(parts * (W + 1) * C * sizeof(float));
 }
 
-// 16-byte vectors of channels: every row of every tensor starts on a 16-byte boundary.
-bool short_conv_vec(int C, int dtype, const void* const* ptrs, int np, const long long* lds, int nl) {
-    const int es = dtype == KDA_BF16 ? 2 : 4;
-    if ((long long)C * es % 16) return false;
+// Four channels at a time: every row of every tensor starts on a boundary of four values
+// (the taps on 16 bytes).
+static bool short_conv_vec(int C, int dtype, const void* w, const void* const* ptrs, int np, const long long* lds, int nl) {
+    const int bytes = dtype == KDA_BF16 ? 8 : 16;
+    if (C % 4 || !mix::al16(w)) return false;
     for (int i = 0; i < np; ++i)
-        if (!mix::al16(ptrs[i])) return false;
+        if (reinterpret_cast<uintptr_t>(ptrs[i]) % bytes) return false;
     for (int i = 0; i < nl; ++i)
-        if (lds[i] * es % 16) return false;
+        if (lds[i] % 4) return false;
     return true;
 }
 
@@ -572,9 +618,9 @@ int launch_short_conv_fwd(const void* x, long long ldx, const void* w, const flo
     a.x = x; a.ldx = ldx; a.w = w; a.bias = bias; a.y = y; a.ldy = ldy;
     a.cache_in = cache_in; a.cache_out = cache_out;
     a.cu = cu; a.nseq = nseq; a.seq_len = seq_len; a.ntok = ntok; a.C = C; a.silu = silu;
-    const void* ptrs[] = {x, w, y, cache_in, cache_out};
+    const void* ptrs[] = {x, y, cache_in, cache_out};
     const long long lds[] = {ldx, ldy};
-    const bool vec = short_conv_vec(C, dtype, ptrs, 5, lds, 2);
+    const bool vec = short_conv_vec(C, dtype, w, ptrs, 4, lds, 2);
     KDA_CONV_DISPATCH((conv::fwd<T, kW>(a, vec, st)))
 }
 
@@ -588,9 +634,9 @@ int launch_short_conv_bwd(const void* dy, long long lddy, const void* x, long lo
     a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
     a.part = static_cast<float*>(ws);
     a.cu = cu; a.nseq = nseq; a.seq_len = seq_len; a.ntok = ntok; a.C = C; a.silu = silu;
-    const void* ptrs[] = {x, w, dy, dx, cache_in, dcache_out};
+    const void* ptrs[] = {x, dy, dx, cache_in, dcache_out};
     const long long lds[] = {ldx, lddy, lddx};
-    const bool vec = short_conv_vec(C, dtype, ptrs, 6, lds, 3);
+    const bool vec = short_conv_vec(C, dtype, w, ptrs, 5, lds, 3);
     KDA_CONV_DISPATCH((conv::bwd<T, kW>(a, vec, dw, db, st)))
 }
 
@@ -599,9 +645,9 @@ int launch_short_conv_step(const void* x, long long ldx, const void* w, const fl
     conv::Args a{};
     a.x = x; a.ldx = ldx; a.w = w; a.bias = bias; a.y = y; a.ldy = ldy;
     a.nseq = B; a.seq_len = 1; a.ntok = B; a.C = C; a.silu = silu;
-    const void* ptrs[] = {x, w, y, cache};
+    const void* ptrs[] = {x, y, cache};
     const long long lds[] = {ldx, ldy};
-    const bool vec = short_conv_vec(C, dtype, ptrs, 4, lds, 2);
+    const bool vec = short_conv_vec(C, dtype, w, ptrs, 3, lds, 2);
     KDA_CONV_DISPATCH((conv::step<T, kW>(a, vec, cache, st)))
 }
 

@@ -2,6 +2,8 @@
 // linear epilogue gradients, short convolution, selective scan).
 #pragma once
 
+#include <type_traits>
+
 #include "kda_common.cuh"
 
 namespace kda {
@@ -149,6 +151,20 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 __device__ __forceinline__ void cp_async_wait0() { cp_async_wait<0>(); }
 
 __device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// Sequence of token t, packed (cu[n] <= t < cu[n + 1]) or dense with seq_len tokens each,
+// and a sequence's first token.
+__device__ __forceinline__ int seq_of(const int32_t* cu, int nseq, int seq_len, int t) {
+    if (!cu) return t / seq_len;
+    int lo = 0, hi = nseq;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+__device__ __forceinline__ int seq_begin(const int32_t* cu, int seq_len, int n) { return cu ? cu[n] : n * seq_len; }
+
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
@@ -190,4 +206,23 @@ inline void sum_parts(const float* part, int parts, long long stride, Out* out, 
 }
 
 }  // namespace mix
+
+// Launches of the mixer's kernels (argument checks: kda_mixer_api.cu).
+size_t layer_norm_bwd_workspace_bytes(int M, int N);
+int launch_layer_norm_fwd(const void* x, long long ldx, const float* w, const float* b, void* y, long long ldy,
+                          float* mean, float* rstd, int M, int N, int dtype, float eps, cudaStream_t st);
+int launch_layer_norm_bwd(const void* dy, long long lddy, const void* x, long long ldx, const float* w,
+                          const float* mean, const float* rstd, void* dx, long long lddx, float* dw, float* db, int M,
+                          int N, int dtype, void* ws, cudaStream_t st);
+size_t short_conv_bwd_workspace_bytes(int ntok, int C, int W);
+int launch_short_conv_fwd(const void* x, long long ldx, const void* w, const float* bias, void* y, long long ldy,
+                          const void* cache_in, void* cache_out, const int32_t* cu, int nseq, int seq_len, int ntok,
+                          int C, int W, int dtype, int silu, cudaStream_t st);
+int launch_short_conv_bwd(const void* dy, long long lddy, const void* x, long long ldx, const void* w,
+                          const float* bias, const void* cache_in, const void* dcache_out, void* dx, long long lddx,
+                          void* dw, float* db, void* dcache_in, const int32_t* cu, int nseq, int seq_len, int ntok,
+                          int C, int W, int dtype, int silu, void* ws, cudaStream_t st);
+int launch_short_conv_step(const void* x, long long ldx, const void* w, const float* bias, void* cache, void* y,
+                           long long ldy, int B, int C, int W, int dtype, int silu, cudaStream_t st);
+
 }  // namespace kda

@@ -1,7 +1,7 @@
 // extern "C" entry points of the selective mixer's operators: host-side argument
 // validation, then launches on the caller's stream.  Declared and documented in
 // include/kda.h.
-#include "kda_mixer.cuh"
+#include "kda_scan.cuh"
 
 namespace kda {
 

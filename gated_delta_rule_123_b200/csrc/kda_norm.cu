@@ -231,31 +231,33 @@ __global__ void __launch_bounds__(kTpr)
     }
 }
 
-// Any width and alignment: one block per row, element by element; the second and
+// Any width and alignment: one block or (up to 1024) one warp per row, element by element; the second and
 // third walk over the row hit the caches.
-template <typename T>
+template <typename T, int kTpr>
 __global__ void __launch_bounds__(256)
     fwd_any_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ b,
-                   T* __restrict__ y, long long ldy, float* __restrict__ mean, float* __restrict__ rstd, int N,
+                   T* __restrict__ y, long long ldy, float* __restrict__ mean, float* __restrict__ rstd, int M, int N,
                    float eps) {
     __shared__ float sred[2][8];
-    const long long row = blockIdx.x;
+    const int t = threadIdx.x % kTpr;
+    const long long row = (long long)blockIdx.x * (256 / kTpr) + threadIdx.x / kTpr;
+    if (row >= M) return;  // whole warps; with one row per block the grid is exact
     const T* xr = x + row * ldx;
     float s = 0.f;
-    for (int j = threadIdx.x; j < N; j += 256) s += to_f32<T>(xr[j]);
-    const float mu = row_sum<256>(s, sred[0]) / float(N);
+    for (int j = t; j < N; j += kTpr) s += to_f32<T>(xr[j]);
+    const float mu = row_sum<kTpr>(s, sred[0]) / float(N);
     s = 0.f;
-    for (int j = threadIdx.x; j < N; j += 256) {
+    for (int j = t; j < N; j += kTpr) {
         const float d = to_f32<T>(xr[j]) - mu;
         s += d * d;
     }
-    const float r = 1.f / sqrtf(row_sum<256>(s, sred[1]) / float(N) + eps);
-    if (threadIdx.x == 0) {
+    const float r = 1.f / sqrtf(row_sum<kTpr>(s, sred[1]) / float(N) + eps);
+    if (t == 0) {
         if (mean) mean[row] = mu;
         if (rstd) rstd[row] = r;
     }
     T* yr = y + row * ldy;
-    for (int j = threadIdx.x; j < N; j += 256)
+    for (int j = t; j < N; j += kTpr)
         yr[j] = from_f32<T>((to_f32<T>(xr[j]) - mu) * r * (w ? w[j] : 1.f) + (b ? b[j] : 0.f));
 }
 
@@ -401,25 +403,27 @@ __global__ void __launch_bounds__(kTpr)
 }
 
 // Any width and alignment: dx row by row, then the column sums in a second walk.
-template <typename T>
+template <typename T, int kTpr>
 __global__ void __launch_bounds__(256)
     bwd_any_kernel(const T* __restrict__ dy, long long lddy, const T* __restrict__ x, long long ldx,
                    const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
-                   T* __restrict__ dx, long long lddx, int N) {
+                   T* __restrict__ dx, long long lddx, int M, int N) {
     __shared__ float sred[2][8];
-    const long long row = blockIdx.x;
+    const int t = threadIdx.x % kTpr;
+    const long long row = (long long)blockIdx.x * (256 / kTpr) + threadIdx.x / kTpr;
+    if (row >= M) return;  // whole warps; with one row per block the grid is exact
     const T *xr = x + row * ldx, *dr = dy + row * lddy;
     const float mu = mean[row], r = rstd[row];
     float s0 = 0.f, s1 = 0.f;
-    for (int j = threadIdx.x; j < N; j += 256) {
+    for (int j = t; j < N; j += kTpr) {
         const float c = __fmul_rn(to_f32<T>(dr[j]), w ? w[j] : 1.f);  // rounded as below: c - mean(c) is exactly 0 at N = 1
         s0 += c;
         s1 += c * (to_f32<T>(xr[j]) - mu) * r;
     }
-    s0 = row_sum<256>(s0, sred[0]) / float(N);
-    s1 = row_sum<256>(s1, sred[1]) / float(N);
+    s0 = row_sum<kTpr>(s0, sred[0]) / float(N);
+    s1 = row_sum<kTpr>(s1, sred[1]) / float(N);
     T* dxr = dx + row * lddx;
-    for (int j = threadIdx.x; j < N; j += 256) {
+    for (int j = t; j < N; j += kTpr) {
         const float xh = (to_f32<T>(xr[j]) - mu) * r;
         dxr[j] = from_f32<T>(r * (__fmul_rn(to_f32<T>(dr[j]), w ? w[j] : 1.f) - s0 - xh * s1));
     }
@@ -498,7 +502,8 @@ int fwd(const T* x, long long ldx, const float* w, const float* b, T* y, long lo
 #undef KDA_LN_ROWS
 #undef KDA_LN_FWD
     } else {
-        fwd_any_kernel<T><<<unsigned(M), 256, 0, st>>>(x, ldx, w, b, y, ldy, mean, rstd, N, eps);
+        if (N <= 1024) fwd_any_kernel<T, 32><<<unsigned(cdiv(M, 8)), 256, 0, st>>>(x, ldx, w, b, y, ldy, mean, rstd, M, N, eps);
+        else fwd_any_kernel<T, 256><<<unsigned(M), 256, 0, st>>>(x, ldx, w, b, y, ldy, mean, rstd, M, N, eps);
     }
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -526,7 +531,8 @@ int bwd(const T* dy, long long lddy, const T* x, long long ldx, const float* w, 
         KDA_LN_BWD(512, 4);
 #undef KDA_LN_BWD
     } else {
-        bwd_any_kernel<T><<<unsigned(M), 256, 0, st>>>(dy, lddy, x, ldx, w, mean, rstd, dx, lddx, N);
+        if (N <= 1024) bwd_any_kernel<T, 32><<<unsigned(cdiv(M, 8)), 256, 0, st>>>(dy, lddy, x, ldx, w, mean, rstd, dx, lddx, M, N);
+        else bwd_any_kernel<T, 256><<<unsigned(M), 256, 0, st>>>(dy, lddy, x, ldx, w, mean, rstd, dx, lddx, M, N);
         parts = any_blocks(M);
         if (dw || db)
             bwd_any_cols_kernel<T><<<dim3(unsigned(cdiv(N, 128)), parts), 128, 0, st>>>(dy, lddy, x, ldx, mean, rstd,

@@ -27,163 +27,10 @@
 // segments: a first pass runs all but the last one's recurrence from a zero state (no
 // y) and leaves the end state and sum(D) of each; since the decay over a segment is
 // exp(A sum(D)), the second pass starts each segment from the states before it.
-#include <stdlib.h>
-#include "kda_mixer.cuh"
+#include "kda_scan.cuh"
 
 namespace kda {
-
 namespace scan {
-
-using namespace mix;
-
-constexpr int kTT = 32;   // tokens of a tile
-constexpr int kCh = 32;   // channels of a block
-constexpr int kYP = 40;   // row pitch of the backward pass's tiles of sums (a quad's four rows on different banks)
-
-struct SArgs {
-    const void *u, *dt, *z, *Bm, *Cm, *dy;
-    const float *A, *skip, *bias, *h0;
-    float* hT;
-    void* y;
-    const int32_t* cu;
-    long long ldu, lddt, ldz, ldb, ldc, ldy, lddy;  // elements from token to token
-    int nseq, seq_len;                              // sequences; dense: tokens of each
-    int rows, row_len;  // dense: B rows of T tokens; packed: one row of all tokens
-    int D, G, N, Dg, bpg;  // channels, groups, states, channels per group, blocks per group
-    int softplus;
-    int L, S;              // tokens per segment, segments per row
-    float *seg_h, *seg_d;  // [rows S][D][N] end states from zero, [rows S][D] sums of D
-    // backward
-    const float* dhT;
-    float *ckpt, *ckpt_d, *seg_g;  // states and sums of D at every chunk's start; the reverse maps
-    float *part_bc, *part_a, *part_d;
-    void *du, *ddt, *dz;
-    float* dh0;
-    long long lddu, ldddt, lddz;
-};
-
-template <typename T>
-struct alignas(16) V8 {
-    T v[8];
-};
-template <typename T, int R>
-struct alignas(R * sizeof(T) < 16 ? R * sizeof(T) : 16) VR {
-    T v[R];
-};
-
-// 8 channels of one token: whole vectors, or element by element up to `valid`.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load8(V8<T>& r, const void* base, long long tok, long long ld, int d, int valid) {
-    const T* p = static_cast<const T*>(base) + tok * ld + d;
-    if constexpr (kVec) {
-        if (valid >= 8) {
-            r = *reinterpret_cast<const V8<T>*>(p);
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = i < valid ? p[i] : from_f32<T>(0.f);
-}
-template <typename T, bool kVec>
-__device__ __forceinline__ void store8(void* base, long long tok, long long ld, int d, int valid, const float* f) {
-    T* p = static_cast<T*>(base) + tok * ld + d;
-    if constexpr (kVec) {
-        if (valid >= 8) {
-            V8<T> r;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r.v[i] = from_f32<T>(f[i]);
-            *reinterpret_cast<V8<T>*>(p) = r;
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < valid) p[i] = from_f32<T>(f[i]);
-}
-template <typename T>
-__device__ __forceinline__ void zero8(V8<T>& r) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = from_f32<T>(0.f);
-}
-
-// R states of one token's B or C (states n0 .. n0 + R - 1 of N).
-template <typename T, int R>
-__device__ __forceinline__ void load_states(VR<T, R>& r, const void* base, long long off, int n0, int N, bool vec) {
-    const T* p = static_cast<const T*>(base) + off + n0;
-    if (vec) {
-        r = *reinterpret_cast<const VR<T, R>*>(p);
-    } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i) r.v[i] = n0 + i < N ? p[i] : from_f32<T>(0.f);
-    }
-}
-
-__device__ __forceinline__ float step_size(float raw, int softplus) { return softplus ? softplus_poly(raw) : raw; }
-
-// R fp32 states of (row r of [..][N]) at n0; zero beyond N.
-template <int R>
-__device__ __forceinline__ void load_h(float (&h)[R], const float* p, int n0, int N) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) h[i] = n0 + i < N ? p[n0 + i] : 0.f;
-}
-template <int R>
-__device__ __forceinline__ void store_h(const float (&h)[R], float* p, int n0, int N) {
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (n0 + i < N) p[n0 + i] = h[i];
-}
-
-// v[j] summed over L neighbouring lanes; lane q of them is left with the sum of v[q].
-template <int L>
-__device__ __forceinline__ float lane_transpose_sum(float (&v)[L], int q) {
-#pragma unroll
-    for (int s = L / 2; s >= 1; s /= 2)
-#pragma unroll
-        for (int i = 0; i < s; ++i) {
-            const float keep = q & s ? v[s + i] : v[i], give = q & s ? v[i] : v[s + i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, s);
-        }
-    return v[0];
-}
-
-// What a block works on: segment s of row b, channels d0 .. of group g.
-struct Place {
-    int b, s, g, d0, dend;
-    long long row0, t0, t1;  // tokens on the flattened axis
-};
-__device__ __forceinline__ Place place(const SArgs& a) {
-    Place p;
-    p.b = blockIdx.y / a.S;
-    p.s = blockIdx.y % a.S;
-    p.g = blockIdx.x / a.bpg;
-    p.d0 = p.g * a.Dg + (blockIdx.x % a.bpg) * kCh;
-    p.dend = (p.g + 1) * a.Dg;
-    p.row0 = (long long)p.b * a.row_len;
-    p.t0 = p.row0 + (long long)p.s * a.L;
-    const long long e = p.row0 + a.row_len;
-    p.t1 = p.t0 + a.L < e ? p.t0 + a.L : e;
-    return p;
-}
-
-// State at the start of segment s (token t0, inside a sequence that began at s_beg
-// before t0): the map of the segment that holds s_beg already starts from that
-// sequence's initial state; the maps after it are applied in order.
-template <int R>
-__device__ __forceinline__ void state_before(float (&h)[R], const SArgs& a, const Place& p, long long s_beg, int d,
-                                             int n0, const float (&A2)[R]) {
-    const int sb = int((s_beg - p.row0) / a.L);
-    const long long base = (long long)p.b * a.S;
-    load_h<R>(h, a.seg_h + ((base + sb) * a.D + d) * a.N, n0, a.N);
-    for (int i = sb + 1; i < p.s; ++i) {
-        float e[R];
-        load_h<R>(e, a.seg_h + ((base + i) * a.D + d) * a.N, n0, a.N);
-        const float sd = a.seg_d[(base + i) * a.D + d];
-#pragma unroll
-        for (int r = 0; r < R; ++r) h[r] = ex2(A2[r] * sd) * h[r] + e[r];
-    }
-}
-
-constexpr int kFT = 16;  // tokens of a tile in the forward pass
 
 template <typename T, int NP, bool kOut>
 struct FwdSmem {
@@ -194,104 +41,9 @@ struct FwdSmem {
     int first[kFT], last[kFT];
 };
 
-// A tile of 32 channels of rows [tt, tt + n) into shared memory; columns past `valid` are
-// left as they were (whole vectors) or 0.
-template <typename T, bool kVec, int kTok>
-__device__ __forceinline__ void stage_tile(T (&dst)[kTok][kCh], const void* base, long long tt, int n, long long ld, int d0,
-                                           int valid, int lane) {
-    const T* p = static_cast<const T*>(base) + tt * ld + d0;
-    if constexpr (kVec) {
-        constexpr int kE = 16 / sizeof(T), kRow = kCh / kE;  // vectors of a row
-#pragma unroll
-        for (int i = 0; i < kTok * kRow / 32; ++i) {
-            const int k = (lane + 32 * i) / kRow, v = (lane + 32 * i) % kRow;
-            if (k < n && v * kE < valid) cp_async<16>(&dst[k][v * kE], p + k * ld + v * kE);
-        }
-    } else {
-        T r[kTok];
-#pragma unroll
-        for (int k = 0; k < kTok; ++k) r[k] = k < n && lane < valid ? p[k * ld + lane] : from_f32<T>(0.f);
-#pragma unroll
-        for (int k = 0; k < kTok; ++k) dst[k][lane] = r[k];
-    }
-}
-// The same for a group's NP states of B or C (states past N are 0).
-template <typename T, int NP, int kTok>
-__device__ __forceinline__ void stage_bc(T (&dst)[kTok][NP], const void* base, long long tt, int n, long long ld, long long off,
-                                         int N, bool vec, int lane) {
-    const T* p = static_cast<const T*>(base) + tt * ld + off;
-    if (vec) {
-        constexpr int kE = 16 / sizeof(T), kRow = NP / kE;
-#pragma unroll
-        for (int i = 0; i < (kTok * kRow + 31) / 32; ++i) {
-            const int k = (lane + 32 * i) / kRow, v = (lane + 32 * i) % kRow;
-            if (k < n) cp_async<16>(&dst[k][v * kE], p + k * ld + v * kE);
-        }
-    } else {
-#pragma unroll 4
-        for (int i = lane; i < kTok * NP; i += 32) {
-            const int k = i / NP, m = i % NP;
-            dst[k][m] = k < n && m < N ? p[k * ld + m] : from_f32<T>(0.f);
-        }
-    }
-}
-
-// B (and C) of a tile as fp32, 8 (bf16) or 4 values a step.
-template <typename T, int NP, int kW, int kTok>
-__device__ __forceinline__ void widen_rows(float (&dst)[kTok][kW], int col, const T (&src)[kTok][NP], int lane) {
-    constexpr int kE = 16 / sizeof(T), kAll = kTok * NP / kE;
-#pragma unroll
-    for (int i = 0; i < (kAll + 31) / 32; ++i) {
-        const int e = (lane + 32 * i) * kE, k = e / NP, m = e % NP;
-        if (kAll % 32 == 0 || k < kTok) {
-            float f[kE];
-            unpack16(*reinterpret_cast<const uint4*>(&src[k][m]), f, T());
-#pragma unroll
-            for (int u = 0; u < kE; u += 4)
-                *reinterpret_cast<float4*>(&dst[k][col + m + u]) = make_float4(f[u], f[u + 1], f[u + 2], f[u + 3]);
-        }
-    }
-}
-
-// All NP states of a channel, in pairs; states past N are 0.
-template <int NP>
-__device__ __forceinline__ void load_pairs(f2 (&h)[NP / 2], const float* p, int N) {
-    if (N == NP && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-        for (int i = 0; i < NP / 4; ++i) {
-            const float4 v = reinterpret_cast<const float4*>(p)[i];
-            h[2 * i] = pk(v.x, v.y);
-            h[2 * i + 1] = pk(v.z, v.w);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NP / 2; ++i) h[i] = pk(2 * i < N ? p[2 * i] : 0.f, 2 * i + 1 < N ? p[2 * i + 1] : 0.f);
-    }
-}
-template <int NP>
-__device__ __forceinline__ void store_pairs(const f2 (&h)[NP / 2], float* p, int N) {
-    if (N == NP && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-        for (int i = 0; i < NP / 4; ++i) {
-            float4 v;
-            upk(h[2 * i], v.x, v.y);
-            upk(h[2 * i + 1], v.z, v.w);
-            reinterpret_cast<float4*>(p)[i] = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NP / 2; ++i) {
-            float a, b;
-            upk(h[i], a, b);
-            if (2 * i < N) p[2 * i] = a;
-            if (2 * i + 1 < N) p[2 * i + 1] = b;
-        }
-    }
-}
-
 // kOut false: the map of a segment (end state from zero, sum of D).  kOut true: outputs.
-template <typename T, int NP, bool kVec, bool kOut>
-__global__ void __launch_bounds__(32, 20) fwd_kernel(const SArgs a, bool bc_vec) {
+template <typename T, int NP, int kCopy, bool kOut>
+__global__ void __launch_bounds__(32, NP <= 16 ? 18 : 10) fwd_kernel(const SArgs a, bool bc_vec) {
     constexpr int kP = NP / 2;
     __shared__ __align__(128) FwdSmem<T, NP, kOut> sm;
     const int lane = threadIdx.x;
@@ -331,18 +83,7 @@ __global__ void __launch_bounds__(32, 20) fwd_kernel(const SArgs a, bool bc_vec)
         // with that sequence's initial state; the maps after it are applied in order
         const long long base = (long long)p.b * a.S;
         const int sb = int((s_beg - p.row0) / a.L);
-        load_pairs<NP>(h, a.seg_h + (base + sb) * row + at, a.N);
-        for (int i = sb + 1; i < p.s; ++i) {
-            f2 e[kP];
-            load_pairs<NP>(e, a.seg_h + (base + i) * row + at, a.N);
-            const f2 sd = dup2(a.seg_d[(base + i) * a.D + d]);
-#pragma unroll
-            for (int k = 0; k < kP; ++k) {
-                float x0, x1;
-                upk(mul2(A2[k], sd), x0, x1);
-                h[k] = fma2(pk(ex2(x0), ex2(x1)), h[k], e[k]);
-            }
-        }
+        chain_states<NP>(h, a, base + sb, base + p.s, d, A2);
     } else if (live && !kOut && s_beg == p.t0 && a.h0) {
         load_pairs<NP>(h, a.h0 + n * row + at, a.N);
     }
@@ -351,12 +92,12 @@ __global__ void __launch_bounds__(32, 20) fwd_kernel(const SArgs a, bool bc_vec)
     int buf = 0;
     auto request = [&](long long tt, int w) {
         const int m = int(p.t1 - tt < kFT ? p.t1 - tt : kFT);
-        stage_tile<T, kVec>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
-        stage_tile<T, kVec>(sm.dt[w], a.dt, tt, m, a.lddt, p.d0, valid, lane);
+        stage_tile<T, kCopy>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
+        stage_tile<T, kCopy>(sm.dt[w], a.dt, tt, m, a.lddt, p.d0, valid, lane);
         stage_bc<T, NP>(sm.b[w], a.Bm, tt, m, a.ldb, (long long)p.g * a.N, a.N, bc_vec, lane);
         if constexpr (kOut) {
             stage_bc<T, NP>(sm.c[w], a.Cm, tt, m, a.ldc, (long long)p.g * a.N, a.N, bc_vec, lane);
-            if (a.z) stage_tile<T, kVec>(sm.z[w], a.z, tt, m, a.ldz, p.d0, valid, lane);
+            if (a.z) stage_tile<T, kCopy>(sm.z[w], a.z, tt, m, a.ldz, p.d0, valid, lane);
         }
         cp_async_commit();
     };
@@ -502,8 +243,10 @@ __global__ void __launch_bounds__(256) step_kernel(const SArgs a, float* __restr
 // their way into a ring that only it reads and the next sequence's other inputs in
 // registers.  256 x 4096 x 16 bf16: 25 us, against 42 us with a thread per sequence,
 // which has too few bytes in flight.
+// Blocks an SM: what the registers (and, at 8 states a lane, the ring) allow without spilling.
+__host__ __device__ constexpr int step_blocks(int R) { return R <= 4 ? 4 : 2; }
 template <typename T, int R>
-__global__ void __launch_bounds__(256) step_many_kernel(const SArgs a, float* __restrict__ state, int per) {
+__global__ void __launch_bounds__(256, R <= 4 ? 4 : 2) step_many_kernel(const SArgs a, float* __restrict__ state, int per) {
     constexpr int kRing = 4;
     using V = VR<float, R>;
     __shared__ __align__(16) V ring[kRing][256];
@@ -589,14 +332,6 @@ __global__ void __launch_bounds__(256) step_many_kernel(const SArgs a, float* __
     }
 }
 
-// ---------------------------------------------------------------- host side
-// States per lane of the step and of the backward pass (4 lanes a channel).
-static int states_per_lane(int N) { return N <= 8 ? 2 : (N <= 16 ? 4 : 8); }
-
-// How the tokens are cut: segments of L tokens, S per row.
-struct Cut {
-    int rows, row_len, bpg, L, S;
-};
 static Cut fwd_cut(int B, int T, int D, int G, bool packed) {
     Cut c{};
     c.rows = packed ? 1 : B;
@@ -606,58 +341,37 @@ static Cut fwd_cut(int B, int T, int D, int G, bool packed) {
     // x 16); with segments, 28 warps an SM measured best (14: 430 us, 56: 370 us).
     const long long warps = (long long)c.rows * G * c.bpg, sms = device_sm_count();
     long long S = warps >= 5 * sms ? 1 : cdiv(28 * sms, warps);
-#ifdef KDA_SCAN_TUNE
-    if (getenv("KDA_S")) S = atoi(getenv("KDA_S"));
-#endif
-    const long long most = T / 64 < 64 ? T / 64 : 64;
-    if (S > most) S = most;
-    if (S < 1) S = 1;
-    c.L = int(cdiv(cdiv(T, S), kTT) * kTT);
-    c.S = int(cdiv(T, c.L));
+    cut_row(c, S);
     return c;
 }
 
-static bool vec8_ok(const SArgs& a, int es, const void* const* ptrs, const long long* lds, int n) {
-    if (a.Dg % 8) return false;
-    for (int i = 0; i < n; ++i)
-        if (ptrs[i] && (!al16(ptrs[i]) || (lds[i] * es) % 16)) return false;
-    return true;
-}
-static int padded_states(int N) { return N <= 8 ? 8 : (N <= 16 ? 16 : 32); }
-// B and C by 16-byte vectors: N is what a lane is padded to, and every group's row is aligned.
-static bool bc_whole(const SArgs& a, int es) {
-    return a.N == padded_states(a.N) && al16(a.Bm) && al16(a.Cm) && (a.ldb * es) % 16 == 0 && (a.ldc * es) % 16 == 0;
-}
-// B and C in whole vectors of n states.
-static bool states_ok(const SArgs& a, int es, int n) {
-    const int bytes = n * es < 16 ? n * es : 16;
-    return a.N == 4 * n && reinterpret_cast<uintptr_t>(a.Bm) % bytes == 0 && reinterpret_cast<uintptr_t>(a.Cm) % bytes == 0 &&
-           (a.ldb * es) % bytes == 0 && (a.ldc * es) % bytes == 0;
-}
-
-template <typename T, int NP, bool kVec>
+template <typename T, int NP, int kCopy>
 int fwd_run(const SArgs& a, bool bc, cudaStream_t st) {
     const dim3 grid(a.G * a.bpg, a.rows * a.S);
-    if (a.S > 1) fwd_kernel<T, NP, kVec, false><<<grid, 32, 0, st>>>(a, bc);
-    fwd_kernel<T, NP, kVec, true><<<grid, 32, 0, st>>>(a, bc);
+    if (a.S > 1) fwd_kernel<T, NP, kCopy, false><<<grid, 32, 0, st>>>(a, bc);
+    fwd_kernel<T, NP, kCopy, true><<<grid, 32, 0, st>>>(a, bc);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
-
+template <typename T, int NP>
+int fwd_states(const SArgs& a, cudaStream_t st) {
+    const void* ptrs[] = {a.u, a.dt, a.z};
+    const long long lds[] = {a.ldu, a.lddt, a.ldz};
+    const int copy = copy_bytes(a, sizeof(T), ptrs, lds, 3);
+    const bool bc = bc_whole(a, sizeof(T));
+    if (copy == 16) return fwd_run<T, NP, 16>(a, bc, st);
+    return copy == 4 ? fwd_run<T, NP, 4>(a, bc, st) : fwd_run<T, NP, 0>(a, bc, st);
+}
 template <typename T>
 int fwd(const SArgs& a, cudaStream_t st) {
-    const void* ptrs[] = {a.u, a.dt, a.z, a.y};
-    const long long lds[] = {a.ldu, a.lddt, a.ldz, a.ldy};
-    const bool vec = vec8_ok(a, sizeof(T), ptrs, lds, 4), bc = bc_whole(a, sizeof(T));
-    if (a.N <= 8) return vec ? fwd_run<T, 8, true>(a, bc, st) : fwd_run<T, 8, false>(a, bc, st);
-    if (a.N <= 16) return vec ? fwd_run<T, 16, true>(a, bc, st) : fwd_run<T, 16, false>(a, bc, st);
-    return vec ? fwd_run<T, 32, true>(a, bc, st) : fwd_run<T, 32, false>(a, bc, st);
+    if (a.N <= 8) return fwd_states<T, 8>(a, st);
+    return a.N <= 16 ? fwd_states<T, 16>(a, st) : fwd_states<T, 32>(a, st);
 }
 
 template <typename T, int R>
 int step(const SArgs& a, float* state, cudaStream_t st) {
     const bool full = al16(state) && states_ok(a, sizeof(T), R);
-    // blocks of the walking form: one wave of 4 an SM; it needs several sequences a block
-    const long long cols = cdiv((long long)a.D * 4, 256), fit = 4ll * device_sm_count() / cols, splits = fit > 1 ? fit : 1;
+    // the walking form in one wave of blocks; it needs several sequences a block
+    const long long cols = cdiv((long long)a.D * 4, 256), fit = (long long)step_blocks(R) * device_sm_count() / cols, splits = fit > 1 ? fit : 1;
     if (full && a.rows >= 8 * splits) {
         const int per = int(cdiv(a.rows, splits));
         step_many_kernel<T, R><<<dim3(unsigned(cols), unsigned(cdiv(a.rows, per))), 256, 0, st>>>(a, state, per);
@@ -684,14 +398,6 @@ int step(const SArgs& a, float* state, cudaStream_t st) {
     if ((N) <= 16) { constexpr int R = 4; return CALL; }       \
     constexpr int R = 8;                                       \
     return CALL;
-
-static void scan_cut_args(scan::SArgs& a, const scan::Cut& c) {
-    a.rows = c.rows;
-    a.row_len = c.row_len;
-    a.bpg = c.bpg;
-    a.L = c.L;
-    a.S = c.S;
-}
 
 // Workspace of a segmented call: the segments' end states and sums, and a copy of the
 // initial states for a call that updates them in place (one segment's block writes a

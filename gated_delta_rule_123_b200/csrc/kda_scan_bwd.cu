@@ -26,7 +26,7 @@
 // the latency of 8 warps an SM: the registers hold KC tokens' decays and states.
 // Measured at 2 x 2047 tokens, 2048 channels, 16 states: 93 us the first pass, 280 us
 // the second (a quad of lanes to a channel: 164 and 633 us).
-#include "kda_mixer.cuh"
+#include "kda_scan.cuh"
 
 namespace kda {
 namespace scan {
@@ -61,7 +61,7 @@ struct MapSmem {
 // The first pass, in the forward pass's layout (a lane holds a channel): states before
 // every KC tokens from a zero state, the sums of D up to there, the segment's end state
 // and its reverse map.
-template <typename T, int NP, bool kVec>
+template <typename T, int NP, int kCopy>
 __global__ void __launch_bounds__(32) bwd_map_kernel(const SArgs a, bool bc_vec) {
     constexpr int kP = NP / 2, KC = ckpt_tokens(NP);
     __shared__ __align__(128) MapSmem<T, NP> sm;
@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(32) bwd_map_kernel(const SArgs a, bool bc_vec)
     long long s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
     auto request = [&](long long tt, int w) {
         const int m = int(p.t1 - tt < kFT ? p.t1 - tt : kFT);
-        stage_tile<T, kVec>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
-        stage_tile<T, kVec>(sm.dt[w], a.dt, tt, m, a.lddt, p.d0, valid, lane);
-        stage_tile<T, kVec>(sm.dy[w], a.dy, tt, m, a.lddy, p.d0, valid, lane);
-        if (a.z) stage_tile<T, kVec>(sm.z[w], a.z, tt, m, a.ldz, p.d0, valid, lane);
+        stage_tile<T, kCopy>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
+        stage_tile<T, kCopy>(sm.dt[w], a.dt, tt, m, a.lddt, p.d0, valid, lane);
+        stage_tile<T, kCopy>(sm.dy[w], a.dy, tt, m, a.lddy, p.d0, valid, lane);
+        if (a.z) stage_tile<T, kCopy>(sm.z[w], a.z, tt, m, a.ldz, p.d0, valid, lane);
         stage_bc<T, NP>(sm.b[w], a.Bm, tt, m, a.ldb, (long long)p.g * a.N, a.N, bc_vec, lane);
         stage_bc<T, NP>(sm.c[w], a.Cm, tt, m, a.ldc, (long long)p.g * a.N, a.N, bc_vec, lane);
         cp_async_commit();
@@ -273,7 +273,7 @@ __device__ __forceinline__ int swz(int lane, int i) {
 }
 
 // The second pass for up to 16 states: a lane holds a channel.
-template <typename T, int NP, bool kVec>
+template <typename T, int NP, int kCopy>
 __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
     constexpr int kP = NP / 2, KC = ckpt_tokens(NP), kV = NP / 4;
     using Smem = MainSmem<T, NP>;
@@ -304,11 +304,6 @@ __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
                 store_pairs<NP>(e, a.dh0 + n * row + at, a.N);
             }
     if (p.t0 >= p.t1) return;
-    auto decay = [&](f2 A, f2 x) {
-        float x0, x1;
-        upk(mul2(A, x), x0, x1);
-        return pk(ex2(x0), ex2(x1));
-    };
     // the state that enters the segment, and the gradient that enters at its end
     const int nf = seq_of(a.cu, a.nseq, a.seq_len, int(p.t0));
     const long long f_beg = seq_begin(a.cu, a.seq_len, nf), f_end = seq_begin(a.cu, a.seq_len, nf + 1);
@@ -318,15 +313,7 @@ __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
         for (int i = 0; i < kP; ++i) h[i] = 0ull;
         const long long base = (long long)p.b * a.S;
         if (live && f_beg < p.t0) {
-            const int sb = int((f_beg - p.row0) / a.L);
-            load_pairs<NP>(h, a.seg_h + (base + sb) * row + at, a.N);
-            for (int i = sb + 1; i < p.s; ++i) {
-                f2 e[kP];
-                load_pairs<NP>(e, a.seg_h + (base + i) * row + at, a.N);
-                const f2 sd = dup2(a.seg_d[(base + i) * a.D + d]);
-#pragma unroll
-                for (int k = 0; k < kP; ++k) h[k] = fma2(decay(A2[k], sd), h[k], e[k]);
-            }
+            chain_states<NP>(h, a, base + (f_beg - p.row0) / a.L, base + p.s, d, A2);
         }
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
@@ -340,16 +327,26 @@ __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
         if (live && l_end > p.t1) {
 #pragma unroll
             for (int k = 0; k < kP; ++k) h[k] = dup2(1.f);  // the decay from t1 to the segment looked at
-            for (int i = p.s + 1; i < a.S; ++i) {
+            // segments up to the one that holds the sequence's end, the next map on its way
+            const int last = int((l_end - 1 - p.row0) / a.L);
+            f2 next[kP];
+            float nsd = 0.f;
+            auto request = [&](int i) {
+                load_pairs<NP>(next, a.seg_g + (base + i) * row + at, a.N);
+                nsd = a.seg_d[(base + i) * a.D + d];
+            };
+            request(p.s + 1);
+            for (int i = p.s + 1; i <= last; ++i) {
                 f2 e[kP];
-                load_pairs<NP>(e, a.seg_g + (base + i) * row + at, a.N);
-                const f2 sd = dup2(a.seg_d[(base + i) * a.D + d]);
+#pragma unroll
+                for (int k = 0; k < kP; ++k) e[k] = next[k];
+                const f2 sd = dup2(nsd);
+                if (i < last) request(i + 1);
 #pragma unroll
                 for (int k = 0; k < kP; ++k) {
                     g[k] = fma2(h[k], e[k], g[k]);
                     h[k] = mul2(h[k], decay(A2[k], sd));
                 }
-                if (l_end <= p.row0 + (long long)(i + 1) * a.L) break;
             }
         }
     }
@@ -365,10 +362,10 @@ __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
     const long long chunk0 = si * (a.L / KC);
     auto request = [&](long long tt, int w) {
         const int m = int(p.t1 - tt < kMT ? p.t1 - tt : kMT);
-        stage_tile<T, kVec>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
-        stage_tile<T, kVec>(sm.dt[w], a.dt, tt, m, a.lddt, p.d0, valid, lane);
-        stage_tile<T, kVec>(sm.dy[w], a.dy, tt, m, a.lddy, p.d0, valid, lane);
-        if (a.z) stage_tile<T, kVec>(sm.z[w], a.z, tt, m, a.ldz, p.d0, valid, lane);
+        stage_tile<T, kCopy>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
+        stage_tile<T, kCopy>(sm.dt[w], a.dt, tt, m, a.lddt, p.d0, valid, lane);
+        stage_tile<T, kCopy>(sm.dy[w], a.dy, tt, m, a.lddy, p.d0, valid, lane);
+        if (a.z) stage_tile<T, kCopy>(sm.z[w], a.z, tt, m, a.ldz, p.d0, valid, lane);
         stage_bc<T, NP>(sm.b[w], a.Bm, tt, m, a.ldb, (long long)p.g * a.N, a.N, bc_vec, lane);
         stage_bc<T, NP>(sm.c[w], a.Cm, tt, m, a.ldc, (long long)p.g * a.N, a.N, bc_vec, lane);
         if (live)
@@ -814,21 +811,57 @@ __global__ void __launch_bounds__(128) bwd_quad_kernel(const SArgs a, bool bc_ve
     }
 }
 
-// dB and dC from the blocks' sums [block][token][group][2][N].
+// The last sums, each in a fixed order, in one launch: dB and dC from the blocks' sums
+// [block][token][group][2][N] (1024 outputs a block, threads side by side), then 32
+// columns a block of dA, dDskip and dbias from the segments'.
 template <typename T>
-__global__ void __launch_bounds__(256) bwd_bc_sum_kernel(const float* __restrict__ part, int parts, long long total,
-                                                         int G, int N, T* __restrict__ dB, long long lddb,
-                                                         T* __restrict__ dC, long long lddc) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
-    float t = 0.f;
+__global__ void __launch_bounds__(1024) bwd_finish_kernel(const SArgs a, const BwdOut o, int bc_blocks, int a_blocks) {
+    __shared__ float s[32][33];
+    if (int(blockIdx.x) < bc_blocks) {
+        const long long total = (long long)a.rows * a.row_len * a.G * 2 * a.N;
+        const long long i = (long long)blockIdx.x * 1024 + threadIdx.x;
+        if (i >= total) return;
+        float t = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < parts; ++k) t += part[k * total + i];
-    const int n = int(i % N);
-    const long long r = i / N, tg = r >> 1;
-    const long long tok = tg / G, g = tg % G;
-    if (r & 1) dC[tok * lddc + g * N + n] = from_f32<T>(t);
-    else dB[tok * lddb + g * N + n] = from_f32<T>(t);
+        for (int k = 0; k < a.bpg; ++k) t += a.part_bc[k * total + i];
+        const int n = int(i % a.N);
+        const long long r = i / a.N, tg = r >> 1, tok = tg / a.G, g = tg % a.G;
+        if (r & 1) static_cast<T*>(o.dC)[tok * o.lddc + g * a.N + n] = from_f32<T>(t);
+        else static_cast<T*>(o.dB)[tok * o.lddb + g * a.N + n] = from_f32<T>(t);
+        return;
+    }
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, b = blockIdx.x - bc_blocks;
+    const int per = (a.D + 31) / 32;  // blocks of a vector of channels
+    const float* part;
+    float* out;
+    long long n, stride, i;
+    if (b < a_blocks) {
+        part = a.part_a;
+        out = o.dA;
+        n = stride = (long long)a.D * a.N;
+        i = (long long)b * 32 + lane;
+    } else {
+        const int which = (b - a_blocks) / per;
+        part = a.part_d + which * a.D;
+        out = which ? o.dbias : o.dskip;
+        n = a.D;
+        stride = 2ll * a.D;
+        i = (long long)((b - a_blocks) % per) * 32 + lane;
+    }
+    if (!out) return;
+    float t = 0.f;
+    if (i < n) {
+#pragma unroll 8
+        for (int k = row; k < a.rows * a.S; k += 32) t += part[k * stride + i];
+    }
+    s[row][lane] = t;
+    __syncthreads();
+    if (row == 0 && i < n) {
+        t = 0.f;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) t += s[r][lane];
+        out[i] = t;
+    }
 }
 
 // Segments of the backward pass: the map pass runs in any case (checkpoints), so they
@@ -843,14 +876,7 @@ static Cut bwd_cut(int B, int T, int D, int G, int N, bool packed) {
     // warps (8192 tokens of 4096 channels in all: 8 segments 380 us, 12 485 us, 16 394 us).
     // Above, 4 blocks of 4 warps an SM.
     long long S = N <= 16 ? 8ll * device_sm_count() / blocks : cdiv(4ll * device_sm_count(), blocks);
-#ifdef KDA_SCAN_TUNE
-    if (getenv("KDA_SB")) S = atoi(getenv("KDA_SB"));
-#endif
-    const long long most = T / 64 < 64 ? T / 64 : 64;
-    if (S > most) S = most;
-    if (S < 1) S = 1;
-    c.L = int(cdiv(cdiv(T, S), kTT) * kTT);
-    c.S = int(cdiv(T, c.L));
+    cut_row(c, S);
     return c;
 }
 
@@ -881,44 +907,38 @@ static BwdPlan bwd_plan(int B, int T, int D, int G, int N, bool packed) {
     return p;
 }
 
-struct BwdOut {
-    void *dB, *dC;
-    long long lddb, lddc;
-    float *dA, *dskip, *dbias;
-};
-
-template <typename T, int NP, bool kVec>
-int bwd_run(const SArgs& a, const BwdOut& o, bool bc, cudaStream_t st) {
+template <typename T, int NP, int kCopy>
+int bwd_run(const SArgs& a, const BwdOut& o, bool bc, bool vec, cudaStream_t st) {
     const dim3 grid(a.G * a.bpg, a.rows * a.S);
-    bwd_map_kernel<T, NP, kVec><<<grid, 32, 0, st>>>(a, bc);
+    bwd_map_kernel<T, NP, kCopy><<<grid, 32, 0, st>>>(a, bc);
     if constexpr (NP <= 16) {
-        auto kern = bwd_kernel<T, NP, kVec>;
+        auto kern = bwd_kernel<T, NP, kCopy>;
         if (!set_smem_attr(kern, sizeof(MainSmem<T, NP>))) return KDA_ERR_CUDA;
         kern<<<grid, 32, sizeof(MainSmem<T, NP>), st>>>(a, bc);
     } else {
-        auto kern = bwd_quad_kernel<T, NP / 4, kVec>;
+        auto kern = vec ? bwd_quad_kernel<T, NP / 4, true> : bwd_quad_kernel<T, NP / 4, false>;
         if (!set_smem_attr(kern, sizeof(BwdSmem<NP / 4>))) return KDA_ERR_CUDA;
         kern<<<grid, 128, sizeof(BwdSmem<NP / 4>), st>>>(a, states_ok(a, sizeof(T), NP / 4));
     }
-    const long long total = (long long)a.rows * a.row_len * a.G * 2 * a.N;
-    bwd_bc_sum_kernel<T><<<unsigned(cdiv(total, 256)), 256, 0, st>>>(a.part_bc, a.bpg, total, a.G, a.N,
-                                                                     static_cast<T*>(o.dB), o.lddb,
-                                                                     static_cast<T*>(o.dC), o.lddc);
-    const int segs = a.rows * a.S;
-    const long long dn = (long long)a.D * a.N;
-    sum_parts<float>(a.part_a, segs, dn, o.dA, nullptr, dn, st);
-    sum_parts<float>(a.part_d, segs, 2ll * a.D, o.dskip, o.dbias, a.D, st);
+    const long long bc_blocks = cdiv((long long)a.rows * a.row_len * a.G * 2 * a.N, 1024);
+    const long long a_blocks = cdiv((long long)a.D * a.N, 32);
+    bwd_finish_kernel<T><<<unsigned(bc_blocks + a_blocks + 2 * cdiv(a.D, 32)), 1024, 0, st>>>(a, o, int(bc_blocks), int(a_blocks));
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-template <typename T>
-int bwd(const SArgs& a, const BwdOut& o, cudaStream_t st) {
+template <typename T, int NP>
+int bwd_states(const SArgs& a, const BwdOut& o, cudaStream_t st) {
     const void* ptrs[] = {a.u, a.dt, a.z, a.dy, a.du, a.ddt, a.dz};
     const long long lds[] = {a.ldu, a.lddt, a.ldz, a.lddy, a.lddu, a.ldddt, a.lddz};
+    const int copy = copy_bytes(a, sizeof(T), ptrs, lds, 4);  // of the inputs
     const bool vec = vec8_ok(a, sizeof(T), ptrs, lds, 7), bc = bc_whole(a, sizeof(T));
-    if (a.N <= 8) return vec ? bwd_run<T, 8, true>(a, o, bc, st) : bwd_run<T, 8, false>(a, o, bc, st);
-    if (a.N <= 16) return vec ? bwd_run<T, 16, true>(a, o, bc, st) : bwd_run<T, 16, false>(a, o, bc, st);
-    return vec ? bwd_run<T, 32, true>(a, o, bc, st) : bwd_run<T, 32, false>(a, o, bc, st);
+    if (copy == 16) return bwd_run<T, NP, 16>(a, o, bc, vec, st);
+    return copy == 4 ? bwd_run<T, NP, 4>(a, o, bc, vec, st) : bwd_run<T, NP, 0>(a, o, bc, vec, st);
+}
+template <typename T>
+int bwd(const SArgs& a, const BwdOut& o, cudaStream_t st) {
+    if (a.N <= 8) return bwd_states<T, 8>(a, o, st);
+    return a.N <= 16 ? bwd_states<T, 16>(a, o, st) : bwd_states<T, 32>(a, o, st);
 }
 
 }  // namespace scan
