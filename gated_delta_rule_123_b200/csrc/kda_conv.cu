@@ -79,13 +79,13 @@ __device__ void tail_rows(const Args& a, long long i0, long long step) {
     const long long total = (long long)a.nseq * a.C;
     for (long long i = i0; i < total; i += step) {
         const int n = int(i / a.C), c = int(i % a.C);
-        const int s0 = seq_begin(a.cu, a.seq_len, n), e0 = seq_begin(a.cu, a.seq_len, n + 1);
+        const int s0 = seq_begin(a.cu, a.seq_len, n, a.ntok), e0 = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
         T r[W - 1];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int p = e0 - (W - 1) + j;
             r[j] = p >= s0 ? x[(long long)p * a.ldx + c]
-                           : (in ? in[((size_t)n * (W - 1) + (W - 1 + p - s0)) * a.C + c] : from_f32<T>(0.f));
+                           : (in ? in[((size_t)n * (W - 1) + max(0, W - 1 + p - s0)) * a.C + c] : from_f32<T>(0.f));
         }
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) out[((size_t)n * (W - 1) + j) * a.C + c] = r[j];
@@ -154,14 +154,14 @@ __global__ void __launch_bounds__(128, kFwdBlocks) fwd_kernel(const Args a, int 
         for (int u = 0; u < kP; ++u) v[u] = kE > 1 ? pk(f[2 * u], f[kE > 1 ? 2 * u + 1 : 0]) : pk(f[0], 0.f);
     };
     int n = seq_of(a.cu, a.nseq, a.seq_len, t0);
-    int s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
+    int s_beg = seq_begin(a.cu, a.seq_len, n, a.ntok), s_end = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
     auto history = [&](int t) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int p = t - (W - 1) + j;
             Row<T, kVec> r;
             if (p >= s_beg) r.load(x + (long long)p * a.ldx);
-            else if (in) r.load(in + ((size_t)n * (W - 1) + (W - 1 + p - s_beg)) * a.C + c0);
+            else if (in) r.load(in + ((size_t)n * (W - 1) + max(0, W - 1 + p - s_beg)) * a.C + c0);
             else r.zero();
             get2(r, h[j]);
         }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(128, kFwdBlocks) fwd_kernel(const Args a, int 
                 while (t >= s_end && n + 1 < a.nseq) {
                     ++n;
                     s_beg = s_end;
-                    s_end = seq_begin(a.cu, a.seq_len, n + 1);
+                    s_end = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
                 }
                 history(t);
             }
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(128, bwd_blocks(Row<T, kVec>::kN))
         for (int j = 0; j < W; ++j) aw[j][u] = 0.f;
     }
     int n = seq_of(a.cu, a.nseq, a.seq_len, t0);
-    int s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
+    int s_beg = seq_begin(a.cu, a.seq_len, n, a.ntok), s_end = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
     float h[W - 1][kE];   // inputs at t-(W-1) .. t-1
     float g[W - 1][kE];   // gradients of the inputs at t-(W-1) .. t-1, as far as they are known
     auto history = [&](int t) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(128, bwd_blocks(Row<T, kVec>::kN))
             const int p = t - (W - 1) + j;
             Row<T, kVec> r;
             if (p >= s_beg) r.load(x + (long long)p * a.ldx);
-            else if (in) r.load(in + ((size_t)n * (W - 1) + (W - 1 + p - s_beg)) * a.C + c0);
+            else if (in) r.load(in + ((size_t)n * (W - 1) + max(0, W - 1 + p - s_beg)) * a.C + c0);
             else r.zero();
             r.get(h[j]);
 #pragma unroll
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(128, bwd_blocks(Row<T, kVec>::kN))
         float f[kE];
 #pragma unroll
         for (int u = 0; u < kE; ++u) f[u] = v[u];
-        if (dout && p >= s_end - (W - 1)) {
+        if (dout && p >= s_end - (W - 1) && p < s_end) {
             Row<T, kVec> r;
             float e[kE];
             r.load(dout + ((size_t)n * (W - 1) + (p - (s_end - (W - 1)))) * a.C + c0);
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(128, bwd_blocks(Row<T, kVec>::kN))
                 while (t >= s_end && n + 1 < a.nseq) {
                     ++n;
                     s_beg = s_end;
-                    s_end = seq_begin(a.cu, a.seq_len, n + 1);
+                    s_end = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
                 }
                 history(t);
             }
@@ -400,7 +400,7 @@ __device__ void cache_gradient(const Args& a, int n, int c) {
 #pragma unroll
     for (int j = 0; j < W; ++j) w[j] = to_f32<T>(static_cast<const T*>(a.w)[(size_t)c * W + j]);
     const float b = a.bias ? a.bias[c] : 0.f;
-    const int s0 = seq_begin(a.cu, a.seq_len, n), e0 = seq_begin(a.cu, a.seq_len, n + 1);
+    const int s0 = seq_begin(a.cu, a.seq_len, n, a.ntok), e0 = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
     float h[2 * W - 2], g[W - 1];  // inputs from position s0 - (W - 1) on; the cache's gradient
 #pragma unroll
     for (int i = 0; i < 2 * W - 2; ++i) {

@@ -152,7 +152,8 @@ __device__ __forceinline__ void cp_async_wait0() { cp_async_wait<0>(); }
 
 __device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 // Sequence of token t, packed (cu[n] <= t < cu[n + 1]) or dense with seq_len tokens each,
-// and a sequence's first token.
+// and a sequence's first token.  Offsets outside 0 .. ntok count as the nearer bound, so
+// that no offsets lead to memory that is not the tensors'.
 __device__ __forceinline__ int seq_of(const int32_t* cu, int nseq, int seq_len, int t) {
     if (!cu) return t / seq_len;
     int lo = 0, hi = nseq;
@@ -163,7 +164,9 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int nseq, int seq_len, 
     }
     return lo;
 }
-__device__ __forceinline__ int seq_begin(const int32_t* cu, int seq_len, int n) { return cu ? cu[n] : n * seq_len; }
+__device__ __forceinline__ int seq_begin(const int32_t* cu, int seq_len, int n, int ntok) {
+    return cu ? max(0, min(cu[n], ntok)) : n * seq_len;
+}
 
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -287,7 +287,7 @@ int kda_selective_scan_fwd(const void* u, long long ldu, const void* dt, long lo
     a.u = u; a.ldu = ldu; a.dt = dt; a.lddt = lddt; a.Bm = B; a.ldb = ldb; a.Cm = C; a.ldc = ldc; a.z = z; a.ldz = ldz;
     a.A = params->A; a.skip = params->D; a.bias = params->dt_bias; a.softplus = params->dt_softplus != 0;
     a.h0 = initial_state; a.hT = final_state; a.y = y; a.ldy = ldy;
-    a.cu = cu_seqlens; a.nseq = nseq; a.seq_len = T; a.D = D; a.G = G; a.N = N; a.Dg = D / G;
+    a.cu = cu_seqlens; a.nseq = nseq; a.seq_len = T; a.ntok = tokens; a.D = D; a.G = G; a.N = N; a.Dg = D / G;
     return launched(launch_selective_scan_fwd(a, batch, T, dtype, workspace, s));
 }
 
@@ -352,7 +352,7 @@ int kda_selective_scan_bwd(const void* dy, long long lddy, const void* u, long l
     a.A = params->A; a.skip = params->D; a.bias = params->dt_bias; a.softplus = params->dt_softplus != 0;
     a.h0 = initial_state; a.dhT = d_final_state; a.dh0 = d_initial_state;
     a.du = du; a.lddu = lddu; a.ddt = ddt; a.ldddt = ldddt; a.dz = z ? dz : nullptr; a.lddz = lddz;
-    a.cu = cu_seqlens; a.nseq = nseq; a.seq_len = T; a.D = D; a.G = G; a.N = N; a.Dg = D / G;
+    a.cu = cu_seqlens; a.nseq = nseq; a.seq_len = T; a.ntok = tokens; a.D = D; a.G = G; a.N = N; a.Dg = D / G;
     const scan::BwdOut o{dB, dC, lddb, lddc, dA, dD, ddt_bias};
     return launched(launch_selective_scan_bwd(a, o, batch, T, dtype, workspace, s));
 }

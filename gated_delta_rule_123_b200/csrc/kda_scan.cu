@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(32, NP <= 16 ? 18 : 10) fwd_kernel(const SArgs
     if (!kOut) {  // only what the segment after this one needs
         if (p.s == a.S - 1) return;
         const int n = seq_of(a.cu, a.nseq, a.seq_len, int(p.t1 - 1));
-        const long long sbeg = seq_begin(a.cu, a.seq_len, n);
+        const long long sbeg = seq_begin(a.cu, a.seq_len, n, a.ntok);
         if (sbeg > p.t0) p.t0 = sbeg;
     }
     f2 A2[kP], h[kP];
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(32, NP <= 16 ? 18 : 10) fwd_kernel(const SArgs
     const size_t at = (size_t)d * a.N, row = (size_t)a.D * a.N;  // of a [channels][N] state
     if (kOut && a.hT)  // empty sequences hand their initial state on
         for (int n = blockIdx.y; n < a.nseq; n += gridDim.y)
-            if (live && seq_begin(a.cu, a.seq_len, n) == seq_begin(a.cu, a.seq_len, n + 1)) {
+            if (live && seq_begin(a.cu, a.seq_len, n, a.ntok) == seq_begin(a.cu, a.seq_len, n + 1, a.ntok)) {
                 f2 e[kP];
 #pragma unroll
                 for (int i = 0; i < kP; ++i) e[i] = 0ull;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(32, NP <= 16 ? 18 : 10) fwd_kernel(const SArgs
             }
     if (p.t0 >= p.t1) return;
     int n = seq_of(a.cu, a.nseq, a.seq_len, int(p.t0));
-    long long s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
+    long long s_beg = seq_begin(a.cu, a.seq_len, n, a.ntok), s_end = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
     if (live && kOut && s_beg < p.t0) {
         // the state at t0: the map of the segment that holds the sequence's start begins
         // with that sequence's initial state; the maps after it are applied in order
@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(32, NP <= 16 ? 18 : 10) fwd_kernel(const SArgs
             int f = -1, l = -1;
             if (lane < steps) {
                 const int m = seq_of(a.cu, a.nseq, a.seq_len, int(tt + lane));
-                if (seq_begin(a.cu, a.seq_len, m) == tt + lane) f = m;
-                if (seq_begin(a.cu, a.seq_len, m + 1) == tt + lane + 1) l = m;
+                if (seq_begin(a.cu, a.seq_len, m, a.ntok) == tt + lane) f = m;
+                if (seq_begin(a.cu, a.seq_len, m + 1, a.ntok) == tt + lane + 1) l = m;
             }
             sm.first[lane] = f;
             sm.last[lane] = l;
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(32, NP <= 16 ? 18 : 10) fwd_kernel(const SArgs
         }
         if (kOut && s_end <= tt + kFT && tt + kFT < p.t1) {
             n = seq_of(a.cu, a.nseq, a.seq_len, int(tt + kFT));
-            s_beg = seq_begin(a.cu, a.seq_len, n);
-            s_end = seq_begin(a.cu, a.seq_len, n + 1);
+            s_beg = seq_begin(a.cu, a.seq_len, n, a.ntok);
+            s_end = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
         }
         __syncwarp();
     }

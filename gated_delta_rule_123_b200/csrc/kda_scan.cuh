@@ -20,7 +20,7 @@ struct SArgs {
     void* y;
     const int32_t* cu;
     long long ldu, lddt, ldz, ldb, ldc, ldy, lddy;  // elements from token to token
-    int nseq, seq_len;                              // sequences; dense: tokens of each
+    int nseq, seq_len, ntok;                        // sequences; dense: tokens of each; all tokens
     int rows, row_len;  // dense: B rows of T tokens; packed: one row of all tokens
     int D, G, N, Dg, bpg;  // channels, groups, states, channels per group, blocks per group
     int softplus;

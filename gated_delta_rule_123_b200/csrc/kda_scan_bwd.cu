@@ -41,8 +41,8 @@ __device__ __forceinline__ void edge_flags(const SArgs& a, long long t, bool her
     first = last = -1;
     if (here) {
         const int m = seq_of(a.cu, a.nseq, a.seq_len, int(t));
-        if (seq_begin(a.cu, a.seq_len, m) == t) first = m;
-        if (seq_begin(a.cu, a.seq_len, m + 1) == t + 1) last = m;
+        if (seq_begin(a.cu, a.seq_len, m, a.ntok) == t) first = m;
+        if (seq_begin(a.cu, a.seq_len, m + 1, a.ntok) == t + 1) last = m;
     }
 }
 
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(32) bwd_map_kernel(const SArgs a, bool bc_vec)
     bool open = true;  // no sequence has ended in the segment yet: later tokens do not see the incoming state
     float dsum = 0.f;
     int n = seq_of(a.cu, a.nseq, a.seq_len, int(p.t0));
-    long long s_beg = seq_begin(a.cu, a.seq_len, n), s_end = seq_begin(a.cu, a.seq_len, n + 1);
+    long long s_beg = seq_begin(a.cu, a.seq_len, n, a.ntok), s_end = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
     auto request = [&](long long tt, int w) {
         const int m = int(p.t1 - tt < kFT ? p.t1 - tt : kFT);
         stage_tile<T, kCopy>(sm.u[w], a.u, tt, m, a.ldu, p.d0, valid, lane);
@@ -182,8 +182,8 @@ __global__ void __launch_bounds__(32) bwd_map_kernel(const SArgs a, bool bc_vec)
         }
         if (s_end <= tt + kFT && tt + kFT < p.t1) {
             n = seq_of(a.cu, a.nseq, a.seq_len, int(tt + kFT));
-            s_beg = seq_begin(a.cu, a.seq_len, n);
-            s_end = seq_begin(a.cu, a.seq_len, n + 1);
+            s_beg = seq_begin(a.cu, a.seq_len, n, a.ntok);
+            s_end = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
         }
         __syncwarp();
     }
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
     const float bias = a.bias && live ? a.bias[d] : 0.f, skip = a.skip && live ? a.skip[d] : 0.f;
     if (a.dh0)  // empty sequences hand the final state's gradient on
         for (int n = blockIdx.y; n < a.nseq; n += gridDim.y)
-            if (live && seq_begin(a.cu, a.seq_len, n) == seq_begin(a.cu, a.seq_len, n + 1)) {
+            if (live && seq_begin(a.cu, a.seq_len, n, a.ntok) == seq_begin(a.cu, a.seq_len, n + 1, a.ntok)) {
                 f2 e[kP];
 #pragma unroll
                 for (int i = 0; i < kP; ++i) e[i] = 0ull;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
     if (p.t0 >= p.t1) return;
     // the state that enters the segment, and the gradient that enters at its end
     const int nf = seq_of(a.cu, a.nseq, a.seq_len, int(p.t0));
-    const long long f_beg = seq_begin(a.cu, a.seq_len, nf), f_end = seq_begin(a.cu, a.seq_len, nf + 1);
+    const long long f_beg = seq_begin(a.cu, a.seq_len, nf, a.ntok), f_end = seq_begin(a.cu, a.seq_len, nf + 1, a.ntok);
     {
         f2 h[kP];
 #pragma unroll
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
             *reinterpret_cast<ulonglong2*>(&sm.hin[swz<NP>(lane, i)]) = v;
         }
         const int nl = seq_of(a.cu, a.nseq, a.seq_len, int(p.t1 - 1));
-        const long long l_end = seq_begin(a.cu, a.seq_len, nl + 1);
+        const long long l_end = seq_begin(a.cu, a.seq_len, nl + 1, a.ntok);
         if (live && l_end > p.t1) {
 #pragma unroll
             for (int k = 0; k < kP; ++k) h[k] = dup2(1.f);  // the decay from t1 to the segment looked at
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(128) bwd_quad_kernel(const SArgs a, bool bc_ve
     }
     if (a.dh0)  // empty sequences hand the final state's gradient on
         for (int n = blockIdx.y; n < a.nseq; n += gridDim.y)
-            if (live && seq_begin(a.cu, a.seq_len, n) == seq_begin(a.cu, a.seq_len, n + 1)) {
+            if (live && seq_begin(a.cu, a.seq_len, n, a.ntok) == seq_begin(a.cu, a.seq_len, n + 1, a.ntok)) {
                 float e[R];
 #pragma unroll
                 for (int r = 0; r < R; ++r) e[r] = 0.f;
@@ -595,11 +595,11 @@ __global__ void __launch_bounds__(128) bwd_quad_kernel(const SArgs a, bool bc_ve
     if (p.t0 >= p.t1) return;  // (never: every segment has tokens)
     // the state that enters the segment, and the gradient that enters at its end
     const int nf = seq_of(a.cu, a.nseq, a.seq_len, int(p.t0));
-    const long long f_beg = seq_begin(a.cu, a.seq_len, nf), f_end = seq_begin(a.cu, a.seq_len, nf + 1);
+    const long long f_beg = seq_begin(a.cu, a.seq_len, nf, a.ntok), f_end = seq_begin(a.cu, a.seq_len, nf + 1, a.ntok);
     if (live && f_beg < p.t0) state_before<R>(hin, a, p, f_beg, d, n0, A2);
     {
         const int nl = seq_of(a.cu, a.nseq, a.seq_len, int(p.t1 - 1));
-        const long long l_end = seq_begin(a.cu, a.seq_len, nl + 1);
+        const long long l_end = seq_begin(a.cu, a.seq_len, nl + 1, a.ntok);
         if (live && l_end > p.t1) {
             float prod[R];
 #pragma unroll

@@ -589,9 +589,9 @@ int kda_short_conv_step(const void *x, long long ldx, const void *w, const float
  * kda_selective_scan_bwd: given dy and d_final_state (or NULL), writes du, ddt, dz
  * [B, T, channels] (dz when z is given), dB, dC [B, T, groups, state], all of the
  * dtype; dA fp32 [channels, state], dD and ddt_bias fp32 [channels] or NULL,
- * d_initial_state fp32 or NULL.  Workspace: per token, channels x state / 2 bytes
- * of states (state 16) and groups x state x channels / (4 x groups) bytes of partial
- * sums; see kda_selective_scan_bwd_workspace().
+ * d_initial_state fp32 or NULL.  Workspace, per token: about 4 bytes of states per
+ * channel and state / 4 (at 9 to 16 states; half of that up to 8, as much above) and
+ * state x channels / 4 bytes of partial sums; kda_selective_scan_bwd_workspace().
  *
  * kda_selective_scan_step: one token for each of B sequences, state [B, channels,
  * state] updated in place; u, dt, z, y [B, channels], B, C [B, groups, state].
