@@ -241,8 +241,7 @@ __global__ void __launch_bounds__(256) step_kernel(const SArgs a, float* __restr
 // The same for many sequences (whole 16-byte vectors of states): a thread keeps its
 // channel's A, bias and skip and walks the sequences b0 .. b1, the next kRing states on
 // their way into a ring that only it reads and the next sequence's other inputs in
-// registers.  256 x 4096 x 16 bf16: 25 us, against 42 us with a thread per sequence,
-// which has too few bytes in flight.
+// registers.  (A thread per sequence: 42 us at 256 x 4096 x 16 bf16.)
 // Blocks an SM: what the registers (and, at 8 states a lane, the ring) allow without spilling.
 __host__ __device__ constexpr int step_blocks(int R) { return R <= 4 ? 4 : 2; }
 template <typename T, int R>
@@ -278,57 +277,60 @@ __global__ void __launch_bounds__(256, R <= 4 ? 4 : 2) step_many_kernel(const SA
     };
 #pragma unroll
     for (int k = 0; k < kRing - 1; ++k) request(k);
-    // the other inputs of the next sequence, by pointers that step from one to the next
-    const T *pu = static_cast<const T*>(a.u) + b0 * a.ldu + d, *pd = static_cast<const T*>(a.dt) + b0 * a.lddt + d;
-    const T* pz = a.z ? static_cast<const T*>(a.z) + b0 * a.ldz + d : nullptr;
+    // Four sequences at a time: each lane of a quad makes one's step size and finishes one's
+    // output, so that the four lanes share that work.
+    auto mine = [&](int b) { return min(b + q, b1 - 1); };
+    T nu, ndt, nz = from_f32<T>(0.f);
+    auto load = [&](int b) {
+        const long long m = mine(b);
+        nu = static_cast<const T*>(a.u)[m * a.ldu + d];
+        ndt = static_cast<const T*>(a.dt)[m * a.lddt + d];
+        if (a.z) nz = static_cast<const T*>(a.z)[m * a.ldz + d];
+    };
     const T *pB = static_cast<const T*>(a.Bm) + b0 * a.ldb + (long long)g * a.N + n0;
     const T *pC = static_cast<const T*>(a.Cm) + b0 * a.ldc + (long long)g * a.N + n0;
-    T* py = static_cast<T*>(a.y) + b0 * a.ldy + d;
-    T nu, ndt, nz = from_f32<T>(0.f);
-    VR<T, R> nB, nC;
-    auto load = [&]() {
-        nu = *pu;
-        ndt = *pd;
-        if (pz) {
-            nz = *pz;
-            pz += a.ldz;
-        }
+    VR<T, R> nB, nC;  // of the next sequence
+    auto load_bc = [&]() {
         nB = *reinterpret_cast<const VR<T, R>*>(pB);
         nC = *reinterpret_cast<const VR<T, R>*>(pC);
-        pu += a.ldu;
-        pd += a.lddt;
         pB += a.ldb;
         pC += a.ldc;
     };
-    if (b0 < b1) load();
-    int slot = 0;
-    for (int b = b0; b < b1; ++b) {
-        const float u = to_f32<T>(nu), raw = to_f32<T>(ndt) + bias, z = to_f32<T>(nz);
-        const VR<T, R> B = nB, C = nC;
-        if (b + 1 < b1) load();
-        cp_async_wait<kRing - 2>();
-        V h = ring[slot][tid];
-        request(slot == 0 ? kRing - 1 : slot - 1);  // into the place of the state before this one
-        if (++slot == kRing) slot = 0;
-        const float D = step_size(raw, a.softplus), w = D * u;
+    if (b0 < b1) {
+        load(b0);
+        load_bc();
+    }
+    for (int b = b0; b < b1; b += 4) {
+        const float u = to_f32<T>(nu), z = to_f32<T>(nz);
+        const float Dq = step_size(to_f32<T>(ndt) + bias, a.softplus), wq = Dq * u;
+        if (b + 4 < b1) load(b + 4);
         float y = 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            h.v[r] = ex2(D * A2[r]) * h.v[r] + w * to_f32<T>(B.v[r]);
-            y += h.v[r] * to_f32<T>(C.v[r]);
-        }
-        y += __shfl_xor_sync(0xffffffffu, y, 1);
-        y += __shfl_xor_sync(0xffffffffu, y, 2);
-        if (live) {
-            *reinterpret_cast<V*>(hp) = h;
-            if (q == 0) {
-                y += skip * u;
-                if (pz) y *= siluf(z);
-                *py = from_f32<T>(y);
+        for (int j = 0; j < 4; ++j) {
+            if (b + j >= b1) break;  // the same for the whole block
+            const VR<T, R> B = nB, C = nC;
+            if (b + j + 1 < b1) load_bc();
+            cp_async_wait<kRing - 2>();
+            V h = ring[j][tid];
+            request((j + 3) & 3);  // into the place of the state before this one
+            const float D = __shfl_sync(0xffffffffu, Dq, j, 4), w = __shfl_sync(0xffffffffu, wq, j, 4);
+            float s = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                h.v[r] = ex2(D * A2[r]) * h.v[r] + w * to_f32<T>(B.v[r]);
+                s += h.v[r] * to_f32<T>(C.v[r]);
             }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            if (q == j) y = s;
+            if (live) *reinterpret_cast<V*>(hp) = h;
+            hp += row;
         }
-        hp += row;
-        py += a.ldy;
+        if (live && b + q < b1) {
+            y += skip * u;
+            if (a.z) y *= siluf(z);
+            static_cast<T*>(a.y)[(long long)(b + q) * a.ldy + d] = from_f32<T>(y);
+        }
     }
 }
 

@@ -59,6 +59,14 @@ def test_norm(kda, M, N, dtype):
     _check(kda, x, dy, w, b, dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N", [(4737, 536), (5001, 1024), (4800, 2048), (4741, 1800), (4739, 4096), (9001, 600)])
+def test_norm_of_many_rows(kda, M, N, dtype):
+    """Enough rows for the kernel whose blocks walk over them."""
+    x, dy, w, b = _inputs(M, N, dtype, M + N)
+    _check(kda, x, dy, w, b, dtype)
+
+
 @pytest.mark.parametrize("N,ld,off", [(256, 264, 8), (256, 300, 0), (250, 257, 3)])
 def test_norm_of_slices(kda, N, ld, off):
     x, dy, w, b = _inputs(19, N, torch.bfloat16, 5, ld, off)

@@ -159,6 +159,21 @@ def test_step_continues_the_sequence(kda, B, ch, G, N, dtype):
     assert_close(state, fin, torch.float32, tol)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,ch,G,N", [(75, 4096, 1, 16), (73, 4096, 2, 8), (41, 4096, 1, 32), (150, 2080, 4, 16), (74, 4093, 1, 16)])
+def test_step_of_many_sequences(kda, B, ch, G, N, dtype):
+    """Enough sequences for the kernel whose threads walk over them; the last one goes without a gate."""
+    c = make(B, 1, ch, G, N, None, dtype, B + N, gate=ch != 4093)
+    d = {k: None if v is None else v.double() for k, v in c.items()}
+    one = lambda k: None if c[k] is None else c[k][:, 0].cuda()  # noqa: E731
+    state = c["h0"].cuda()
+    y = kda.selective_scan_step(one("u"), one("dt"), c["A"].cuda(), one("Bm"), one("Cm"), state, c["D"].cuda(), one("z"),
+                                c["bias"].cuda())
+    want, fin = ref.scan(d["u"], d["dt"], d["A"], d["Bm"], d["Cm"], d["D"], d["z"], d["bias"], True, d["h0"])
+    assert_close(y, want[:, 0], dtype, 20 * 2.0 ** -20)
+    assert_close(state, fin, torch.float32, 20 * 2.0 ** -20)
+
+
 def test_no_tokens_and_state_in_place(kda):
     e = torch.empty((2, 0, 16), device="cuda")
     A, bc = -torch.ones((16, 4), device="cuda"), torch.empty((2, 0, 1, 4), device="cuda")
