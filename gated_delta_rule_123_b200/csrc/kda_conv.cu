@@ -8,8 +8,8 @@
 // The inputs before a sequence's start come from its cache of W - 1 rows, oldest
 // first, or are zero.  Dense batches and packed sequences are one axis of tokens,
 // on which the window restarts at each sequence.  Bound by HBM: forward reads x
-// and writes y, backward reads dy and x and writes dx.  A thread owns one 16-byte
-// vector of channels and slides over a run of tokens, so each row is read once
+// and writes y, backward reads dy and x and writes dx.  A thread owns four
+// channels (8 bytes of bf16, 16 of fp32) and slides over a run of tokens, so each row is read once
 // but for the W - 1 rows next to the run.
 #include "kda_mixer.cuh"
 
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(128) step_kernel(const Args a, T* __restrict__
 
 // Tokens of one thread in the forward pass: one wave of the blocks that the SMs hold
 // (65536 x 4096 bf16 in 3.5 waves of shorter runs 224 us, in 7 waves 308 us, in one 194 us
-// = 5.5 TB/s).
+// = 5.5 TB/s at best; other machines 223).
 static int fwd_run(int ntok, int C, int kE) {
     const long long want = cdiv((long long)ntok * cdiv(C, kE), (long long)device_sm_count() * kFwdBlocks * 128);
     return int(want < 8 ? 8 : want);

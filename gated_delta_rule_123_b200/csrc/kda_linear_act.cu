@@ -31,7 +31,7 @@ template <int kBN, bool kPre>
 struct LPlan {
     static constexpr uint32_t kB = kBN * BK * 2, kStage = kABytes + kB;
     // per epilogue warp: one tile, for s and then for y (a tile for each would cost the
-    // fourth stage: 516 us against 400 at 16384 x 8192 x 2048 with the pre-activation)
+    // fourth stage: 516 us against 424 at 16384 x 8192 x 2048 with a bias and the pre-activation)
     static constexpr uint32_t kStagingBytes = 4096;
     // as many stages as fit beside the staging tiles and the barriers, at most 8
     static constexpr int kFit = int((232448 - 1280 - kEpiWarps * kStagingBytes) / kStage);
@@ -64,9 +64,8 @@ __device__ __forceinline__ void store_ragged(__nv_bfloat16* row, const float* v,
 // 1 - Phi(|x|) = erfc(|x| / sqrt 2) / 2 and e^{-x^2/2}.  erfc(z) = e^{-z^2} t S(t) with t =
 // 1 / (1 + z / 2); S is a polynomial fitted to a relative 1.4e-6 over z in [0, 10], beyond
 // which the product is below the smallest bf16.  Relative accuracy in the tail matters
-// (x Phi(x) for negative x), so erf's absolute error bounds would not do; and the
-// two-branch erff made the epilogue, not the tensor cores, the bound of a wide GELU
-// projection (16384 x 8192 x 2048: 552 us, now 399).
+// (x Phi(x) for negative x), so erf's absolute error bounds would not do.  At
+// 16384 x 8192 x 2048 with a bias, GELU takes 411 us where no activation takes 385.
 __device__ __forceinline__ float phi_tail(float x, float& gauss) {
     const float z = fabsf(x) * 0.70710678118654752f;
     const float t = mix::rcp(fmaf(0.5f, z, 1.f));
@@ -470,7 +469,7 @@ __device__ __forceinline__ float act1(float x, int act) {
 // 16 bytes that it copies into a ring of kU steps and reads back itself, with no
 // exchange between threads.  (Loads into registers do not stay in flight: the compiler
 // sinks them to their MMAs, 54 registers where kU steps would need 96.)  128-row tiles of
-// the kernel above leave most SMs idle and 112 of 128 rows empty: 32 us at 16 x 2048 x 4096.
+// the kernel above leave most SMs idle and 112 of 128 rows empty: 32 us at 16 x 2048 x 4096, here 6 to 8.
 constexpr int kSkinnyWarps = 8;
 template <int kMT>
 struct Skinny {

@@ -176,7 +176,7 @@ inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 // add every 32nd part each, then their sums are added.  Two outputs of n columns side
 // by side in the parts (n each, the second may be NULL) go in one launch.  Bound by
 // the latency of a thread's chain of loads, so the chain is short and unrolled:
-// 592 parts of 4096 columns take 4 us (with 8 threads a column, 20 us).
+// 592 parts of 4096 columns take 6 us (with 8 threads a column, 20 us).
 template <typename Out>
 __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, int parts, long long stride,
                                                          Out* __restrict__ out, Out* __restrict__ out2, long long n) {

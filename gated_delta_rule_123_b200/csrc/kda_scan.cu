@@ -18,8 +18,8 @@
 // the N states are N independent chains, which hide each other's latency; and B and C
 // are the same for the whole warp: one broadcast 16-byte read of shared memory serves
 // four states of 32 channels.  (Four or eight lanes to a channel, for more warps from
-// the same channels, measured 480 us at 8192 tokens x 4096 channels x 16 states where
-// this layout takes 365: the exchange and the per-lane copies of D and D u made the
+// the same channels, measured 455 us at best at 8192 tokens x 4096 channels x 16 states
+// where this layout takes 372: the exchange and the per-lane copies of D and D u made the
 // shared-memory pipe and the instruction issue the bound.)  u, dt, z, B and C are
 // copied a tile of 16 tokens ahead into shared memory by cp.async.
 //
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(256) step_kernel(const SArgs a, float* __restr
 // The same for many sequences (whole 16-byte vectors of states): a thread keeps its
 // channel's A, bias and skip and walks the sequences b0 .. b1, the next kRing states on
 // their way into a ring that only it reads and the next sequence's other inputs in
-// registers.  (A thread per sequence: 42 us at 256 x 4096 x 16 bf16.)
+// registers.  256 x 4096 x 16 bf16: 28 us = 5.1 TB/s (a thread per sequence: 42 us).
 // Blocks an SM: what the registers (and, at 8 states a lane, the ring) allow without spilling.
 __host__ __device__ constexpr int step_blocks(int R) { return R <= 4 ? 4 : 2; }
 template <typename T, int R>

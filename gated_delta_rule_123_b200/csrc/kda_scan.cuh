@@ -289,9 +289,6 @@ __device__ __forceinline__ void chain_states(f2 (&h)[NP / 2], const SArgs& a, lo
 }
 
 // ---------------------------------------------------------------- host side
-// States per lane of the step and of the backward pass (4 lanes a channel).
-inline int states_per_lane(int N) { return N <= 8 ? 2 : (N <= 16 ? 4 : 8); }
-
 // How the tokens are cut: segments of L tokens, S per row.
 struct Cut {
     int rows, row_len, bpg, L, S;

@@ -24,7 +24,7 @@
 // channels for dB and dC are the only exchange; they go through shared memory, then
 // over the blocks in a fixed order: every result is the same on every run.  Bound by
 // the latency of 8 warps an SM: the registers hold KC tokens' decays and states.
-// Measured at 2 x 2047 tokens, 2048 channels, 16 states: 93 us the first pass, 280 us
+// Measured at 2 x 2047 tokens, 2048 channels, 16 states: 98 us the first pass, 285 us
 // the second (a quad of lanes to a channel: 164 and 633 us).
 #include "kda_scan.cuh"
 
