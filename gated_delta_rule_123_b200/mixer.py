@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 
 import torch
 
@@ -142,6 +143,22 @@ def _ld_inner(t, what, inner):
         step *= shape[-k]
 
 
+def _sizes(*values):
+    """Refuse what the library's int arguments cannot hold (a conversion would cut it off)."""
+    if max(values) > 0x7fffffff:
+        raise ValueError("sizes and the projection's row strides must be below 2^31")
+
+
+def _ld32(t, what):
+    """Row stride for the projection, whose strides are ints; 0 without a tensor."""
+    if t is None:
+        return 0
+    ld = _ld(t, what)
+    if ld > 0x7fffffff:
+        _sizes(ld)
+    return ld
+
+
 def _scratch(workspace, need, device):
     if workspace is not None and workspace.numel() * workspace.element_size() >= need:
         if workspace.device != device or not workspace.is_contiguous():
@@ -151,6 +168,7 @@ def _scratch(workspace, need, device):
 
 
 def _seqs(cu_seqlens, B, device):
+    _sizes(B if cu_seqlens is None else cu_seqlens.numel())
     if cu_seqlens is None:
         return 0, B
     if B != 1:
@@ -179,6 +197,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
     mean = torch.empty(lead, device=dev, dtype=torch.float32)
     rstd = torch.empty_like(mean)
     M = mean.numel()
+    _sizes(M, N)
     _run(dev, "kda_layer_norm_fwd", _p(x), _ld(x, "x"), _p(weight), _p(bias), _p(y), _ld(y, "out"), _p(mean), _p(rstd), M,
          N, _CODE[x.dtype], float(eps))
     return y, mean, rstd
@@ -194,6 +213,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, weight_grad=True, bias_grad=True, 
     _whole(mean, "mean", lead, torch.float32, dev)
     _whole(rstd, "rstd", lead, torch.float32, dev)
     M = mean.numel()
+    _sizes(M, N)
     dx = _new(x)
     dw = torch.empty(N, device=dev, dtype=torch.float32) if weight_grad else None
     db = torch.empty(N, device=dev, dtype=torch.float32) if bias_grad else None
@@ -221,6 +241,7 @@ def linear_act(x, W, bias=None, residual=None, act="none", output_pre=False, out
     if x.dim() != 2 or W.dim() != 2:
         raise ValueError("x [M, K] and W [N, K] must have two axes")
     (M, K), N = x.shape, W.shape[0]
+    _sizes(M, N, K)
     _like(W, "W", (N, K), torch.bfloat16, dev)
     _whole(bias, "bias", (N,), torch.float32, dev)
     _like(residual, "residual", (M, N), torch.bfloat16, dev)
@@ -228,8 +249,8 @@ def linear_act(x, W, bias=None, residual=None, act="none", output_pre=False, out
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
     y = _padded(M, N, dev) if out is None else _like(out, "out", (M, N), torch.bfloat16, dev)
     pre = _padded(M, N, dev) if output_pre else None
-    _run(dev, "kda_linear_act_bf16", _p(x), _ld(x, "x"), _p(W), _ld(W, "W"), _p(bias), _p(residual),
-         0 if residual is None else _ld(residual, "residual"), _p(y), _ld(y, "out"), _p(pre),
+    _run(dev, "kda_linear_act_bf16", _p(x), _ld32(x, "x"), _p(W), _ld32(W, "W"), _p(bias), _p(residual),
+         _ld32(residual, "residual"), _p(y), _ld32(y, "out"), _p(pre),
          0 if pre is None else pre.stride(0), M, N, K, ACTIVATIONS[act])
     return (y, pre) if output_pre else y
 
@@ -241,6 +262,7 @@ def linear_act_bwd(dy, x, W, pre=None, act="none", bias_grad=True, workspace=Non
     if x.dim() != 2 or W.dim() != 2:
         raise ValueError("x [M, K] and W [N, K] must have two axes")
     (M, K), N = x.shape, W.shape[0]
+    _sizes(M, N, K)
     _like(W, "W", (N, K), torch.bfloat16, dev)
     _like(dy, "dy", (M, N), torch.bfloat16, dev)
     if act not in ACTIVATIONS:
@@ -248,11 +270,11 @@ def linear_act_bwd(dy, x, W, pre=None, act="none", bias_grad=True, workspace=Non
     if act != "none" and pre is None:
         raise ValueError("pre is required with an activation")
     _like(pre, "pre", (M, N), torch.bfloat16, dev)
+    lddy, ldx, ldw, ldp = _ld32(dy, "dy"), _ld32(x, "x"), _ld32(W, "W"), _ld32(pre, "pre")
     dx, dW = _padded(M, K, dev), _padded(N, K, dev)
     db = torch.empty(N, device=dev, dtype=torch.float32) if bias_grad else None
     ws, n = _scratch(workspace, _query(dev, "kda_linear_act_bwd_workspace", M, N), dev)
-    _run(dev, "kda_linear_act_bwd_bf16", _p(dy), _ld(dy, "dy"), _p(x), _ld(x, "x"), _p(W), _ld(W, "W"), _p(pre),
-         0 if pre is None else _ld(pre, "pre"), _p(dx), dx.stride(0) if M else K, _p(dW), dW.stride(0) if N else K, _p(db),
+    _run(dev, "kda_linear_act_bwd_bf16", _p(dy), lddy, _p(x), ldx, _p(W), ldw, _p(pre), ldp, _p(dx), dx.stride(0) if M else K, _p(dW), dW.stride(0) if N else K, _p(db),
          M, N, K, ACTIVATIONS[act], _p(ws), n)
     return dx, dW, db
 
@@ -264,6 +286,7 @@ def _conv_operands(x, weight, bias, cu_seqlens, conv_state):
         raise ValueError("x [B, T, C] must have three axes and weight [C, width] two")
     B, T, C = x.shape
     W = weight.shape[1]
+    _sizes(B * T, C, W)
     _whole(weight, "weight", (C, W), x.dtype, dev)
     _whole(bias, "bias", (C,), torch.float32, dev)
     nseq, n = _seqs(cu_seqlens, B, dev)
@@ -313,6 +336,7 @@ def short_conv_step(x, weight, conv_state, bias=None, silu=True, out=None):
         raise ValueError("x [B, C] and weight [C, width] must have two axes")
     B, C = x.shape
     W = weight.shape[1]
+    _sizes(B, C, W)
     _whole(weight, "weight", (C, W), x.dtype, dev)
     _whole(bias, "bias", (C,), torch.float32, dev)
     _whole(conv_state, "conv_state", (B, W - 1, C), x.dtype, dev)
@@ -329,6 +353,7 @@ def _scan_operands(u, dt, A, B, C, D, z, dt_bias, dt_softplus):
         raise ValueError("A must be [channels, state] and B [..., groups, state]")
     lead, ch = u.shape[:-1], u.shape[-1]
     G, N = B.shape[-2:]
+    _sizes(math.prod(lead), ch, G, N)
     if G < 1 or ch % G:
         raise ValueError("channels must be a multiple of groups")
     _like(dt, "dt", u.shape, u.dtype, dev)

@@ -584,7 +584,10 @@ int kda_short_conv_step(const void *x, long long ldx, const void *w, const float
  *                  256-byte aligned.
  * States and sums are fp32.  Sequences that are too few for the SMs are cut into
  * segments whose maps are composed; the result is the recurrence's up to rounding,
- * and the same on every run.
+ * and the same on every run.  The recurrence is meant to decay (D_t A <= 0).  Modes
+ * that grow are computed too while the product of a sequence's decays between any
+ * two tokens stays in fp32's range; where it overflows, outputs that are finite step
+ * by step (a state that is still zero) may be NaN.
  *
  * kda_selective_scan_bwd: given dy and d_final_state (or NULL), writes du, ddt, dz
  * [B, T, channels] (dz when z is given), dB, dC [B, T, groups, state], all of the

@@ -137,3 +137,40 @@ def test_row_strides():
             _ld(bad, "t")
     with pytest.raises(ValueError):
         _ld(t.view(3, 5, 2, 12)[:, :, :, :6], "t", 2)
+
+
+def test_sizes_and_strides_past_32_bits_are_refused(kda, monkeypatch):
+    """The C entry points take int sizes (and the projection int row strides): what does not fit never reaches them."""
+    from gated_delta_rule_123_b200 import mixer
+
+    def reached(*args):
+        raise AssertionError("reached the library")
+    monkeypatch.setattr(mixer, "_first", lambda t, what, dtypes=(): t.device)  # tensors without storage stand in
+    monkeypatch.setattr(mixer, "_run", reached)
+    monkeypatch.setattr(mixer, "_query", reached)
+    big, b16, f32 = (1 << 32) + 5, torch.bfloat16, torch.float32
+    m = lambda *s, t=b16: torch.empty(s, device="meta", dtype=t)  # noqa: E731
+    far = torch.empty_strided((2, 8), ((1 << 32) + 8, 1), device="meta", dtype=b16)
+    w, x = m(8, 8), m(2, 8)
+    A = m(1, 1, t=f32)
+    calls = [
+        lambda: mixer.layer_norm_fwd(m(big, 1)),
+        lambda: mixer.layer_norm_bwd(m(big, 1), m(big, 1), None, m(big, t=f32), m(big, t=f32)),
+        lambda: mixer.linear_act(m(big, 8), w), lambda: mixer.linear_act(far, w), lambda: mixer.linear_act(x, far),
+        lambda: mixer.linear_act(x, w, residual=far), lambda: mixer.linear_act(x, w, out=far),
+        lambda: mixer.linear_act_bwd(m(big, 8), m(big, 8), w), lambda: mixer.linear_act_bwd(far, x, w),
+        lambda: mixer.linear_act_bwd(x, far, w), lambda: mixer.linear_act_bwd(x, x, w, far, "silu"),
+        lambda: mixer.short_conv_fwd(m(1, big, 1), m(1, 4)), lambda: mixer.short_conv_fwd(m(big, 1, 1), m(1, 4)),
+        lambda: mixer.short_conv_fwd(m(1 << 16, 1 << 16, 1), m(1, 4)),
+        lambda: mixer.short_conv_bwd(m(1, big, 1), m(1, big, 1), m(1, 4)),
+        lambda: mixer.short_conv_fwd(m(big, 0, 1), m(1, 4)),
+        lambda: mixer.short_conv_fwd(m(1, 4, 1), m(1, 4), cu_seqlens=m(big, t=torch.int32)),
+        lambda: mixer.short_conv_step(m(big, 1), m(1, 4), m(big, 3, 1)),
+        lambda: mixer.selective_scan_fwd(m(1, big, 1), m(1, big, 1), A, m(1, big, 1, 1), m(1, big, 1, 1)),
+        lambda: mixer.selective_scan_bwd(m(1, big, 1), m(1, big, 1), m(1, big, 1), A, m(1, big, 1, 1), m(1, big, 1, 1)),
+        lambda: mixer.selective_scan_step(m(big, 1), m(big, 1), A, m(big, 1, 1), m(big, 1, 1), m(big, 1, 1, t=f32)),
+    ]
+    for i, f in enumerate(calls):
+        with pytest.raises(ValueError, match="2\\^31"):
+            f()
+            raise AssertionError(i)
