@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(128, kFwdBlocks) fwd_kernel(const Args a, int 
     const T* x = static_cast<const T*>(a.x) + c0;
     T* y = static_cast<T*>(a.y) + c0;
     const T* in = static_cast<const T*>(a.cache_in);
-    const int t0 = at * run, t1 = min(a.ntok, t0 + run);
+    const int t0 = at * run, t1 = run < a.ntok - t0 ? t0 + run : a.ntok;  // (t0 + run may pass 2^31)
     Row<T, kVec> ring[kRing];
 #pragma unroll
     for (int j = 0; j < kRing; ++j)
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(128, bwd_blocks(Row<T, kVec>::kN))
     T* dx = static_cast<T*>(a.dx) + c0;
     const T* in = static_cast<const T*>(a.cache_in);
     const T* dout = static_cast<const T*>(a.dcache_out);
-    const int t0 = at * run, t1 = min(a.ntok, t0 + run);
+    const int t0 = at * run, t1 = run < a.ntok - t0 ? t0 + run : a.ntok;  // (t0 + run may pass 2^31)
     float w[kE][W], b[kE], aw[W][kE], ab[kE];
     load_taps<T, W, kE>(static_cast<const T*>(a.w), c0, w);
 #pragma unroll

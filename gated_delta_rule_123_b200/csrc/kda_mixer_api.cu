@@ -11,6 +11,8 @@ static bool aligned_es(const void* p, int dtype) {
     return (reinterpret_cast<uintptr_t>(p) & (dtype == KDA_BF16 ? 1u : 3u)) == 0;
 }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// Row and column counts leave room for the kernels' rounding up in 32 bits.
+static bool too_long(int a, int b, int c = 0) { return a > 0x7fffff00 || b > 0x7fffff00 || c > 0x7fffff00; }
 static int launched(int rc) {
     return rc == KDA_OK ? KDA_OK : fail(rc, cudaGetErrorString(cudaGetLastError()));
 }
@@ -63,6 +65,7 @@ int kda_layer_norm_fwd(const void* x, long long ldx, const float* weight, const 
     t_last_error[0] = 0;
     if (bad_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, "dtype must be KDA_BF16 or KDA_FP32");
     if (M < 0 || N < 1) return fail(KDA_ERR_INVALID_ARG, "M must not be negative and N must be positive");
+    if (too_long(M, N)) return fail(KDA_ERR_UNSUPPORTED, "more than 2^31 - 256 rows or columns");
     if (M == 0) return KDA_OK;
     if (!x || !y) return fail(KDA_ERR_INVALID_ARG, "NULL tensor pointer");
     if (ldx < N || ldy < N) return fail(KDA_ERR_INVALID_ARG, "row stride smaller than the row");
@@ -85,6 +88,7 @@ int kda_layer_norm_bwd(const void* dy, long long lddy, const void* x, long long 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (bad_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, "dtype must be KDA_BF16 or KDA_FP32");
     if (M < 0 || N < 1) return fail(KDA_ERR_INVALID_ARG, "M must not be negative and N must be positive");
+    if (too_long(M, N)) return fail(KDA_ERR_UNSUPPORTED, "more than 2^31 - 256 rows or columns");
     if (!aligned4(weight) || !aligned4(mean) || !aligned4(rstd) || !aligned4(dweight) || !aligned4(dbias))
         return fail(KDA_ERR_INVALID_ARG, "pointers must be aligned to their element type");
     if (M == 0) {
@@ -108,6 +112,7 @@ int kda_linear_act_bf16(const void* x, int ldx, const void* W, int ldw, const fl
                         int ldr, void* y, int ldy, void* pre, int ldp, int M, int N, int K, int act, void* stream) {
     t_last_error[0] = 0;
     if (M < 0 || N < 0 || K < 0) return fail(KDA_ERR_INVALID_ARG, "negative size");
+    if (too_long(M, N, K)) return fail(KDA_ERR_UNSUPPORTED, "more than 2^31 - 256 rows or columns");
     if (act < KDA_ACT_NONE || act > KDA_ACT_SOFTPLUS) return fail(KDA_ERR_INVALID_ARG, "unknown activation");
     if ((long long)M * N == 0) return KDA_OK;
     if (K == 0) return fail(KDA_ERR_UNSUPPORTED, "K must be positive");
@@ -137,6 +142,7 @@ int kda_linear_act_bwd_bf16(const void* dy, int lddy, const void* x, int ldx, co
     t_last_error[0] = 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M < 0 || N < 0 || K < 0) return fail(KDA_ERR_INVALID_ARG, "negative size");
+    if (too_long(M, N, K)) return fail(KDA_ERR_UNSUPPORTED, "more than 2^31 - 256 rows or columns");
     if (act < KDA_ACT_NONE || act > KDA_ACT_SOFTPLUS) return fail(KDA_ERR_INVALID_ARG, "unknown activation");
     if (!aligned4(dbias)) return fail(KDA_ERR_INVALID_ARG, "pointers must be aligned to their element type");
     if (K == 0 && (long long)M * N != 0) return fail(KDA_ERR_UNSUPPORTED, "K must be positive");

@@ -20,6 +20,7 @@ def test_layer_norm(kda, lib):
     assert fwd(dtype=2) == bad and fwd(M=-1) == bad and fwd(N=0) == bad and fwd(x=None) == bad and fwd(y=None) == bad
     assert fwd(ldx=63) == bad and fwd(ldy=63) == bad and fwd(y=P) == bad and fwd(x=P + 1) == bad and fwd(w=P + 2) == bad
     assert fwd(x=P + 2, dtype=1) == bad and fwd(M=0) == kda.KDA_OK
+    assert fwd(M=0x7fffff01) == fwd(N=0x7fffff01, ldx=1 << 31, ldy=1 << 31) == kda.KDA_ERR_UNSUPPORTED
 
     def bwd(dy=P, x=Q, mean=S, rstd=S, dx=R, dw=S, ws=None, size=0, ld=64, M=4):
         return lib.kda_layer_norm_bwd(dy, ld, x, ld, None, mean, rstd, dx, ld, dw, None, M, 64, 0, ws, size, None)
@@ -38,6 +39,7 @@ def test_linear(kda, lib):
     assert fwd(ldx=68) == bad and fwd(y=R + 8) == bad and fwd(ldy=36) == bad and fwd(r=S, ldr=31) == bad
     assert fwd(pre=S, ldp=36) == bad and fwd(pre=S + 2, ldp=40) == bad and fwd(y=P) == bad and fwd(r=R, ldr=32) == bad
     assert fwd(pre=R, ldp=32) == bad and fwd(b=S + 2) == bad and fwd(r=S + 1, ldr=32) == bad
+    assert fwd(M=0x7fffff01) == fwd(N=0x7fffff01) == fwd(K=0x7fffff01) == kda.KDA_ERR_UNSUPPORTED
     assert fwd(K=0, ldx=64) == kda.KDA_ERR_UNSUPPORTED and fwd(M=0) == kda.KDA_OK and fwd(N=0, K=0) == kda.KDA_OK
 
     def bwd(dy=P, lddy=32, x=Q, W=R, pre=S, dx=S + 4096, dW=S + 8192, act=3, ws=None, size=0, K=64, lddx=64):

@@ -237,3 +237,19 @@ def test_more_than_2_31_elements(kda):
     yr, finr = ref.scan(sub(u), sub(dt), d(A[pick]), d(Bm[:, -3000:]), d(Cm[:, -3000:]))
     assert_close(y[:, -200:, pick], yr[:, -200:], torch.bfloat16, (3000 ** 0.5 + 16) * 2.0 ** -20)
     assert_close(fin[:, pick], finr, torch.float32, (3000 ** 0.5 + 16) * 2.0 ** -20)
+
+
+@pytest.mark.slow
+def test_almost_2_31_tokens(kda):
+    """One channel, as many tokens as the convolution takes: the last run ends next to 2^31."""
+    T = 0x7fffff00
+    x = torch.full((1, T, 1), 0.5, device="cuda", dtype=torch.bfloat16)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x[0, -70:] = torch.randn((70, 1), generator=gen, device="cuda").to(torch.bfloat16)
+    w = (0.4 * torch.randn((1, 4), generator=gen, device="cuda")).to(torch.bfloat16)
+    y = torch.full_like(x, float("nan"))
+    kda.short_conv_fwd(x, w, out=y)
+    want = ref.conv(x[:, -70:].double().cpu(), w.double().cpu(), None, None, None, True)[0]
+    assert_close(y[:, -60:], want[:, 10:], torch.bfloat16, 2.0 ** -18)
+    # 2^20 equal tokens before them: the window's sum is the same for each
+    assert torch.equal(y[0, -(1 << 20):-70], y[0, 10:11].expand((1 << 20) - 70, 1))
