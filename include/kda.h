@@ -461,7 +461,10 @@ int kda_layer_decode(const void *x, const kda_layer_weights *w, void *conv_state
  * Conventions on top of those above: token tensors here have a row stride
  * ("ld...", in elements, at least the row), so that a slice of a wider
  * projection can be passed; token t of batch row b is row b*T + t of a
- * dense tensor.  Rows that start on 16-byte boundaries
+ * dense tensor.  cu_seqlens is as in kda_chunk_fwd (0 first, the number of rows
+ * last); offsets outside 0 .. rows count as the nearer bound, and rows that the
+ * offsets leave out have unspecified outputs and count in the gradients' sums.
+ * Rows that start on 16-byte boundaries
  * and divide into 16-byte vectors are the fast path; any other alignment of
  * the element type, stride or width is accepted unless stated.  Outputs must
  * not overlap inputs except where stated.
