@@ -502,14 +502,15 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps)
         const int k = s * 32 + t * 8;
         uint4* v = ring + slot * kV * 32;
         if (s < s1) {
-            const bool in = k < p.K;  // (K is a multiple of 8)
-            if (in && in0) mix::cp_async<16>(v, w0 + k);
+            const bool in = k < p.K;
+            const int bytes = min(16, 2 * (p.K - k));  // (what a row holds after its K values is not read)
+            if (in && in0) mix::cp_async_part(v, w0 + k, bytes);
             else v[0] = zero;
-            if (in && in1) mix::cp_async<16>(v + 32, w1 + k);
+            if (in && in1) mix::cp_async_part(v + 32, w1 + k, bytes);
             else v[32] = zero;
 #pragma unroll
             for (int m = 0; m < kMT; ++m) {
-                if (in && m * 8 + g < p.M) mix::cp_async<16>(v + (2 + m) * 32, x + (size_t)(m * 8 + g) * ldx + k);
+                if (in && m * 8 + g < p.M) mix::cp_async_part(v + (2 + m) * 32, x + (size_t)(m * 8 + g) * ldx + k, bytes);
                 else v[(2 + m) * 32] = zero;
             }
         }

@@ -98,3 +98,39 @@ def test_gradients_of_no_rows(kda):
     dx, dW, db = kda.linear_act_bwd(e(0, 24), e(0, 16), torch.ones(24, 16, device="cuda", dtype=torch.bfloat16), e(0, 24), "silu")
     assert dx.shape == (0, 16) and not dW.any() and not db.any()
     assert kda.linear_act(e(0, 16), e(24, 16)).shape == (0, 24)
+
+
+def _in_padding(t):
+    """t [rows, n] as columns of a tensor whose rows go on with NaN to the next multiple of 8 and 8 more."""
+    rows, n = t.shape
+    full = torch.full((rows, (n + 7) // 8 * 8 + 8), float("nan"), device="cuda", dtype=t.dtype)
+    full[:, :n] = t.cuda()
+    return full[:, :n]
+
+
+@pytest.mark.parametrize("M", [1, 7, 16, 32, 50, 64, 150, 300])
+@pytest.mark.parametrize("N,K", [(24, 1), (40, 12), (17, 31), (264, 100), (33, 1029)])
+def test_sums_that_end_inside_a_vector(kda, M, N, K):
+    """K not a multiple of 8: what a row holds behind its K values takes no part."""
+    gen = torch.Generator().manual_seed(M + N + K)
+    x, W = _t(gen, M, K), _t(gen, N, K, std=K ** -0.5)
+    y = kda.linear_act(_in_padding(x), _in_padding(W))
+    torch.cuda.synchronize()
+    assert kda.device_status() == 0
+    assert_close(y, x.double() @ W.double().T, torch.bfloat16, FP32)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (5, 12, 20), (40, 17, 12), (150, 100, 31), (300, 1029, 33)])
+def test_gradients_whose_sums_end_inside_a_vector(kda, M, N, K, act):
+    gen = torch.Generator().manual_seed(M + N + K)
+    x, W, dy, pre = _t(gen, M, K), _t(gen, N, K, std=K ** -0.5), _t(gen, M, N), _t(gen, M, N)
+    ws = torch.full((1 << 24,), 255, device="cuda", dtype=torch.uint8)  # NaN in every type
+    dx, dW, db = kda.linear_act_bwd(_in_padding(dy), _in_padding(x), _in_padding(W),
+                                    None if act == "none" else _in_padding(pre), act, workspace=ws)
+    torch.cuda.synchronize()
+    assert kda.device_status() == 0
+    ds = dy.double() * ref.act(pre.double(), act)[1]
+    assert_close(dx, ds @ W.double(), torch.bfloat16, FP32 + DS, "dx")
+    assert_close(dW, ds.T @ x.double(), torch.bfloat16, FP32 + DS, "dW")
+    assert_close(db, ds.sum(0), torch.float32, 2.0 ** -18 * M ** 0.5, "db")
