@@ -373,7 +373,16 @@ __global__ void __launch_bounds__(128, bwd_blocks(Row<T, kVec>::kN))
                     s_beg = s_end;
                     s_end = seq_begin(a.cu, a.seq_len, n + 1, a.ntok);
                 }
-                history(t);
+                if (t < s_end) {
+                    history(t);
+                } else {  // rows behind the last offset: their window goes on, but the gradients before them are complete
+                    s_beg = t;
+                    s_end = 0x7fffffff;
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                        for (int u = 0; u < kE; ++u) g[j][u] = 0.f;
+                }
             }
             token(i, t, std::false_type{});
         }
