@@ -41,8 +41,9 @@ __device__ __forceinline__ void edge_flags(const SArgs& a, long long t, bool her
     first = last = -1;
     if (here) {
         const int m = seq_of(a.cu, a.nseq, a.seq_len, int(t));
-        if (seq_begin(a.cu, a.seq_len, m, a.ntok) == t) first = m;
-        if (seq_begin(a.cu, a.seq_len, m + 1, a.ntok) == t + 1) last = m;
+        const int end = seq_begin(a.cu, a.seq_len, m + 1, a.ntok);
+        if (seq_begin(a.cu, a.seq_len, m, a.ntok) == t && end > t) first = m;  // (not an empty one before rows left out)
+        if (end == t + 1) last = m;
     }
 }
 
