@@ -326,7 +326,8 @@ __global__ void __launch_bounds__(kTpr)
         }
         const float mu = nmu, r = nr;
         if (kAhead && row + gridDim.x < M) request(row + gridDim.x);
-        const f2 r2 = dup2(r), nmr = dup2(-mu * r);
+        // (xh from the difference: x r - mu r would cancel where the mean is far above the spread)
+        const f2 r2 = dup2(r), minus_mu = dup2(-mu);
         f2 p0 = 0ull, p1 = 0ull;  // sums of c and c xh
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kTpr)
                 const ulonglong2 ww = weights(i, u);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    const f2 xh = fma2(fx[u + v], r2, nmr), c = mul2(fd[u + v], v ? ww.y : ww.x);
+                    const f2 xh = mul2(add2(fx[u + v], minus_mu), r2), c = mul2(fd[u + v], v ? ww.y : ww.x);
                     p0 = add2(p0, c);
                     p1 = fma2(c, xh, p1);
                     aw[i][u + v] = fma2(fd[u + v], xh, aw[i][u + v]);
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kTpr)
                 const ulonglong2 ww = weights(i, u);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    const f2 xh = fma2(fx[u + v], r2, nmr), c = mul2(fd[u + v], v ? ww.y : ww.x);
+                    const f2 xh = mul2(add2(fx[u + v], minus_mu), r2), c = mul2(fd[u + v], v ? ww.y : ww.x);
                     upk(fma2(c, r2, fma2(xh, m1, m0)), o[2 * (u + v)], o[2 * (u + v) + 1]);
                 }
             }
