@@ -83,13 +83,6 @@ __device__ __forceinline__ float gelu(float x) {
     const float q = phi_tail(x, g);
     return x * (x > 0.f ? 1.f - q : q);
 }
-// softplus with the fast log: the result is rounded to bf16.  Below -8 the sum 1 + e^x
-// keeps too few bits of e^x, and log(1 + e^x) is e^x to within e^x / 2 < 2^-12 of it.
-__device__ __forceinline__ float softplus_bf16(float x) {
-    const float e = __expf(-fabsf(x));
-    return fmaxf(x, 0.f) + (e < 3.3e-4f ? e : __logf(1.f + e));
-}
-
 // Outputs and the residual pass once: stored and loaded as the first lines to leave L2,
 // which W and the rows of x in flight need.
 __device__ __forceinline__ uint64_t policy_evict_first() {
@@ -120,7 +113,7 @@ __device__ __forceinline__ void apply_act(float* v, int act) {
             break;
         case kSoftplus:
 #pragma unroll
-            for (int j = 0; j < kN; ++j) v[j] = softplus_bf16(v[j]);
+            for (int j = 0; j < kN; ++j) v[j] = mix::softplus_poly(v[j]);
             break;
         default: break;
     }
