@@ -551,7 +551,7 @@ int fwd(const Args& a, bool vec, cudaStream_t st) {
         const long long n = cdiv((long long)a.nseq * a.C, 256);
         tail_kernel<T, W><<<unsigned(n < 4096 ? n : 4096), 256, 0, st>>>(a);
     }
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 template <typename T, int W>
@@ -570,7 +570,7 @@ int bwd(const Args& a, bool vec, void* dw, float* db, cudaStream_t st) {
     if (more > 1024) more = 1024;
     if (dw || db || more)
         bwd_finish_kernel<T, W><<<dim3(cols, unsigned(W + 1 + more)), 1024, 0, st>>>(a, parts, static_cast<T*>(dw), db);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 template <typename T, int W>
@@ -579,7 +579,7 @@ int step(const Args& a, bool vec, void* cache, cudaStream_t st) {
     const unsigned grid = unsigned(cdiv((long long)a.nseq * (a.C / kE), 128));
     if (vec) step_kernel<T, W, true><<<grid, 128, 0, st>>>(a, static_cast<T*>(cache));
     else step_kernel<T, W, false><<<grid, 128, 0, st>>>(a, static_cast<T*>(cache));
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // namespace conv

@@ -13,6 +13,7 @@ static bool aligned_es(const void* p, int dtype) {
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 // Row and column counts leave room for the kernels' rounding up in 32 bits.
 static bool too_long(int a, int b, int c = 0) { return a > 0x7fffff00 || b > 0x7fffff00 || c > 0x7fffff00; }
+// (the launchers of the norm, the convolution and the scan leave the runtime's error here to be taken)
 static int launched(int rc) {
     return rc == KDA_OK ? KDA_OK : fail(rc, cudaGetErrorString(cudaGetLastError()));
 }

@@ -506,7 +506,7 @@ int fwd(const T* x, long long ldx, const float* w, const float* b, T* y, long lo
         if (N <= 1024) fwd_any_kernel<T, 32><<<unsigned(cdiv(M, 8)), 256, 0, st>>>(x, ldx, w, b, y, ldy, mean, rstd, M, N, eps);
         else fwd_any_kernel<T, 256><<<unsigned(M), 256, 0, st>>>(x, ldx, w, b, y, ldy, mean, rstd, M, N, eps);
     }
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 template <typename T>
@@ -540,7 +540,7 @@ int bwd(const T* dy, long long lddy, const T* x, long long ldx, const float* w, 
                                                                                         part, M, N);
     }
     sum_parts<float>(part, parts, 2ll * N, dw, db, N, st);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // namespace norm

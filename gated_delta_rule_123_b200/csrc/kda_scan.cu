@@ -352,7 +352,7 @@ int fwd_run(const SArgs& a, bool bc, cudaStream_t st) {
     const dim3 grid(a.G * a.bpg, a.rows * a.S);
     if (a.S > 1) fwd_kernel<T, NP, kCopy, false><<<grid, 32, 0, st>>>(a, bc);
     fwd_kernel<T, NP, kCopy, true><<<grid, 32, 0, st>>>(a, bc);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 template <typename T, int NP>
 int fwd_states(const SArgs& a, cudaStream_t st) {
@@ -382,7 +382,7 @@ int step(const SArgs& a, float* state, cudaStream_t st) {
         if (full) step_kernel<T, R, true><<<grid, 256, 0, st>>>(a, state);
         else step_kernel<T, R, false><<<grid, 256, 0, st>>>(a, state);
     }
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // namespace scan

@@ -924,7 +924,7 @@ int bwd_run(const SArgs& a, const BwdOut& o, bool bc, bool vec, cudaStream_t st)
     const long long bc_blocks = cdiv((long long)a.rows * a.row_len * a.G * 2 * a.N, 1024);
     const long long a_blocks = cdiv((long long)a.D * a.N, 32);
     bwd_finish_kernel<T><<<unsigned(bc_blocks + a_blocks + 2 * cdiv(a.D, 32)), 1024, 0, st>>>(a, o, int(bc_blocks), int(a_blocks));
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 template <typename T, int NP>
