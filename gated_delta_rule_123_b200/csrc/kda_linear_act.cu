@@ -27,7 +27,7 @@ using namespace gemm;  // the GEMM's TMA, TMEM and staging helpers, and its tile
 enum Act { kNone = KDA_ACT_NONE, kRelu = KDA_ACT_RELU, kGelu = KDA_ACT_GELU, kSilu = KDA_ACT_SILU,
            kSoftplus = KDA_ACT_SOFTPLUS };
 
-template <int kBN, bool kPre>
+template <int kBN>
 struct LPlan {
     static constexpr uint32_t kB = kBN * BK * 2, kStage = kABytes + kB;
     // per epilogue warp: one tile, for s and then for y (a tile for each would cost the
@@ -123,7 +123,7 @@ template <int kBN, bool kAMN, bool kBMN, bool kPre>
 __global__ void __launch_bounds__(gemm::kThreads, 1)
     kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
            const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_p, const LArgs p) {
-    using P = LPlan<kBN, kPre>;
+    using P = LPlan<kBN>;
     constexpr int kStages = P::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -408,7 +408,7 @@ static int launch_tile(const void* A, int lda, const void* B, int ldb, void* C, 
     const long long tiles = (long long)a.tiles_m * a.tiles_n;
     const int sms = device_sm_count(), grid = int(tiles < sms ? tiles : sms);
     auto kern = kernel<kBN, kAMN, kBMN, kPre>;
-    constexpr uint32_t smem = LPlan<kBN, kPre>::kSmem;
+    constexpr uint32_t smem = LPlan<kBN>::kSmem;
     if (!set_smem_attr(kern, smem)) {
         *why = "cudaFuncSetAttribute failed for the GEMM kernel";
         return KDA_ERR_CUDA;

@@ -390,7 +390,6 @@ __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
         const int steps = int(p.t1 - tt < kMT ? p.t1 - tt : kMT);
         int ef = -1, el = -1;
         if (lane < kMT) {
-            // (a tile strictly inside the segment's first or last sequence needs no search)
             edge_flags(a, tt + lane, lane < steps, ef, el);
             sm.first[lane] = ef;
             sm.last[lane] = el;
@@ -526,7 +525,7 @@ __global__ void __launch_bounds__(32) bwd_kernel(const SArgs a, bool bc_vec) {
 
 // 2R values per lane summed over the 8 quads of a warp (lanes with the same q): each
 // exchange hands half of the values to the partner, so lane (quad bits b4 b3 b2) is
-// left with value(s) number b4 R + b3 R/2 + ...; returns how many (kLeft).
+// left with the values from number b4 R + b3 R/2 + b2 R/4 on, R/4 of them.
 template <int R>
 __device__ __forceinline__ void channel_sum(float (&v)[2 * R], int lane) {
     const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
@@ -540,14 +539,10 @@ __device__ __forceinline__ void channel_sum(float (&v)[2 * R], int lane) {
         const float keep = b3 ? v[R / 2 + i] : v[i], give = b3 ? v[i] : v[R / 2 + i];
         v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
     }
-    if constexpr (R >= 4) {
 #pragma unroll
-        for (int i = 0; i < R / 4; ++i) {
-            const float keep = b2 ? v[R / 4 + i] : v[i], give = b2 ? v[i] : v[R / 4 + i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
-        }
-    } else {
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 4);
+    for (int i = 0; i < R / 4; ++i) {
+        const float keep = b2 ? v[R / 4 + i] : v[i], give = b2 ? v[i] : v[R / 4 + i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
     }
 }
 
@@ -565,6 +560,7 @@ struct BwdSmem {
 
 template <typename T, int R, bool kVec>
 __global__ void __launch_bounds__(128) bwd_quad_kernel(const SArgs a, bool bc_vec) {
+    static_assert(R == 8, "what a lane is left with of the sums over channels");
     constexpr int KC = ckpt_tokens(4 * R);
     extern __shared__ __align__(16) uint8_t smem_raw[];
     BwdSmem<R>& sm = *reinterpret_cast<BwdSmem<R>*>(smem_raw);
@@ -747,14 +743,8 @@ __global__ void __launch_bounds__(128) bwd_quad_kernel(const SArgs a, bool bc_ve
                     channel_sum<R>(v, lane);
                     // value number b4 R + b3 R/2 + ... of the list [dB | dC] of this lane's states
                     float* o = sm.red[warp][k] + ((lane & 16) ? 4 * R : 0) + n0;
-                    if constexpr (R == 2) {
-                        if (!(lane & 4)) o[(lane >> 3) & 1] = v[0];
-                    } else if constexpr (R == 4) {
-                        o[((lane >> 2) & 2) + ((lane >> 2) & 1)] = v[0];
-                    } else {
-                        o[((lane >> 1) & 4) + ((lane >> 1) & 2)] = v[0];
-                        o[((lane >> 1) & 4) + ((lane >> 1) & 2) + 1] = v[1];
-                    }
+                    o[((lane >> 1) & 4) + ((lane >> 1) & 2)] = v[0];
+                    o[((lane >> 1) & 4) + ((lane >> 1) & 2) + 1] = v[1];
                 }
                 sm.gb[k0 + j4 + q][c] = lane_transpose_sum<4>(agb, q);
                 sm.ea[k0 + j4 + q][c] = lane_transpose_sum<4>(aea, q);
