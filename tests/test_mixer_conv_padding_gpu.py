@@ -13,7 +13,8 @@ TOL = 2.0 ** -18
 
 
 def check(kda, T, C, W, cu, dtype, state, behind, seed, columns=None):
-    """``behind``: the gradient in the rows that the offsets leave out, 0 or 1 (random).  Sums are compared where it is 0."""
+    """``behind``: the gradient in the rows that the offsets leave out: 0, 1 (random), or NaN, there in the inputs too.  Sums
+    are compared where it is 0."""
     gen = torch.Generator().manual_seed(seed)
     n = len(cu) - 1
     r = lambda *s, std=1.0: (std * torch.randn(s, generator=gen)).to(dtype)  # noqa: E731
@@ -22,6 +23,8 @@ def check(kda, T, C, W, cu, dtype, state, behind, seed, columns=None):
     inside = torch.zeros(T, dtype=torch.bool)
     inside[cu[0]:cu[-1]] = True
     dy[0, ~inside] *= behind
+    if behind != behind:
+        x[0, ~inside] = behind
     pick = slice(None) if columns is None else columns
     d = lambda t: None if t is None else t[..., pick].double()  # noqa: E731  (channels are independent)
     c = lambda t: None if t is None else t.cuda()  # noqa: E731
@@ -36,14 +39,14 @@ def check(kda, T, C, W, cu, dtype, state, behind, seed, columns=None):
     assert_close(dx.cpu()[:, inside][..., pick], dxr[:, inside], dtype, TOL, "dx")
     if state:
         assert_close(din.cpu()[..., pick], dinr, dtype, TOL, "dstate")
-    if not behind:
+    if behind == 0:
         assert_close(dw.cpu()[pick], dwr, dtype, TOL * T ** 0.5, "dw")
         assert_close(db.cpu()[pick], dbr, torch.float32, TOL * T ** 0.5, "db")
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("W", [2, 3, 4])
-@pytest.mark.parametrize("behind", [0, 1])
+@pytest.mark.parametrize("behind", [0, 1, float("nan")])
 @pytest.mark.parametrize("cu", [[0, 13, 29], [0, 32], [0, 31], [0, 33], [0, 30, 31], [0, 30, 30, 32, 32], [0, 1], [0, 0],
                                 [0, 39]])
 def test_rows_behind_the_last_sequence(kda, cu, behind, W, dtype):
@@ -59,5 +62,5 @@ def test_rows_behind_the_last_sequence(kda, cu, behind, W, dtype):
 def test_rows_behind_the_last_sequence_in_long_runs(kda, last, C, dtype):
     """6000 rows of 4096 channels: runs of 65 (forward) and 109 tokens; 1025 channels: 65 and 41."""
     columns = torch.arange(0, C, 41)
-    for behind in (0, 1):
+    for behind in (0, 1, float("nan")):
         check(kda, 6000, C, 4, [0, 700, last - 2, last], dtype, True, behind, last + C, columns)
