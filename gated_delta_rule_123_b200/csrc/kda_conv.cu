@@ -20,7 +20,7 @@ namespace conv {
 using namespace mix;
 
 // Four channels of a row (8 bytes of bf16, 16 of fp32), or one.  (Eight bf16 channels a
-// thread need twice the registers: half the warps, or spills.)
+// thread need twice the registers: half the warps, or more spills.)
 template <typename T, bool kVec>
 struct Row {
     static constexpr int kN = kVec ? 4 : 1;
@@ -53,7 +53,9 @@ struct Row {
     __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<type*>(p) = v; }
 };
 
-constexpr int kFwdRing = 10, kFwdBlocks = 5;  // rows in flight a thread, blocks an SM
+// Rows in flight a thread, blocks an SM: chosen for bf16, whose width 4 spills 16 bytes a
+// thread; fp32 rows are twice as wide and spill 192 bytes at width 4 and 60 at width 3.
+constexpr int kFwdRing = 10, kFwdBlocks = 5;
 
 struct Args {
     const void *x, *w, *cache_in;

@@ -63,7 +63,9 @@ __device__ __forceinline__ void store_ragged(__nv_bfloat16* row, const float* v,
 
 // 1 - Phi(|x|) = erfc(|x| / sqrt 2) / 2 and e^{-x^2/2}.  erfc(z) = e^{-z^2} t S(t) with t =
 // 1 / (1 + z / 2); S is a polynomial fitted to a relative 1.4e-6 over z in [0, 10], beyond
-// which the product is below the smallest bf16.  Relative accuracy in the tail matters
+// which the product is below the smallest bf16.  z^2 is rounded before the exponential, so
+// the whole is good to 2e-6 up to |x| = 3 and 1.8e-5 at 13; results are rounded to bf16
+// (3.9e-3).  Relative accuracy in the tail matters
 // (x Phi(x) for negative x), so erf's absolute error bounds would not do.  At
 // 16384 x 8192 x 2048 with a bias, GELU takes 411 us where no activation takes 385.
 __device__ __forceinline__ float phi_tail(float x, float& gauss) {

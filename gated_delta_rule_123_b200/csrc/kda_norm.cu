@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kTpr == 32 ? 128 : kTpr)
 // Many rows of up to 512 vectors: kTpr threads own two vectors of columns each and keep
 // those columns' weight and bias in registers for all the rows that the block walks
 // (read from L1 for every row they are four times the row's own bytes, and the L1 pipe
-// was the bound: 102 us at 65536 x 2048 bf16, now 90 us = 6.0 TB/s).  512 threads an SM
+// was the bound: 102 us at 65536 x 2048 bf16, now 90 us = 6.0 TB/s, in a graph's replays).  512 threads an SM
 // measured best (384: 98, 640: 97, 768: 122 us).  kR rows at a time share the barriers;
 // the rows to come are on their way into a ring by copies that each thread waits for on
 // its own (it reads back only what it copied itself).

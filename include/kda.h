@@ -461,13 +461,16 @@ int kda_layer_decode(const void *x, const kda_layer_weights *w, void *conv_state
  * Conventions on top of those above: token tensors here have a row stride
  * ("ld...", in elements, at least the row), so that a slice of a wider
  * projection can be passed; token t of batch row b is row b*T + t of a
- * dense tensor.  cu_seqlens is as in kda_chunk_fwd (0 first, the number of rows
- * last); offsets outside 0 .. rows count as the nearer bound, and rows that the
- * offsets leave out have unspecified outputs and count in the gradients' sums.
- * Rows that start on 16-byte boundaries
- * and divide into 16-byte vectors are the fast path; any other alignment of
- * the element type, stride or width is accepted unless stated.  Outputs must
- * not overlap inputs except where stated.
+ * dense tensor.  cu_seqlens is as in kda_chunk_fwd (0 first, then non-decreasing),
+ * but a packed buffer may be longer than its sequences: the rows behind
+ * cu_seqlens[num_seqs] belong to none.  Whatever they hold, the sequences' rows,
+ * states and caches and their gradients are what they would be without them.
+ * Their own outputs are unspecified, and their terms count in the sums over rows
+ * (dw, dbias, dA, dD, ddt_bias): give them finite inputs and dy = 0 where those are
+ * wanted.  Offsets outside 0 .. rows count as the nearer bound.
+ * Rows that start on 16-byte boundaries and divide into 16-byte vectors are the
+ * fast path; any other alignment of the element type, stride or width is accepted
+ * unless stated.  Outputs must not overlap inputs except where stated.
  * ======================================================================== */
 
 /* ------------------------------------------------------------------------
@@ -582,7 +585,8 @@ int kda_short_conv_step(const void *x, long long ldx, const void *w, const float
  *   A              fp32 [channels, state];  D, dt_bias fp32 [channels] or NULL.
  *   initial_state / final_state  fp32 [N, channels, state] or NULL (zero / not
  *                  written); they may be the same buffer.
- *   1 <= state <= 32; channels is a multiple of groups.
+ *   1 <= state <= 32; channels is a multiple of groups.  Dense: at most 65535
+ *   sequences (more can be packed; the step takes any number).
  *   workspace      kda_selective_scan_fwd_workspace(...) bytes (0: may be NULL),
  *                  256-byte aligned.
  * States and sums are fp32.  Sequences that are too few for the SMs are cut into
